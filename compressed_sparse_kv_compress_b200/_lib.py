@@ -18,6 +18,7 @@ OVERLAP_PREVIOUS = 1  # csa_compress flags (CSKV_OVERLAP_PREVIOUS)
 ATTN_PAIRS = 0x100  # OR-ed into hybrid_decode_attn's mode (CSKV_ATTN_PAIRS)
 ATTN_KV_FP8 = 0x200  # OR-ed into hybrid_decode_attn's mode (CSKV_ATTN_KV_FP8)
 KV8_ROW_BYTES = 336  # CSKV_KV8_ROW_BYTES
+KV4_ROW_BYTES = 176  # CSKV_KV4_ROW_BYTES
 CSA, HCA = 0, 1
 DEV_BAD_INDEX, DEV_TAIL_MISSING, DEV_CAPACITY, DEV_TIMEOUT = 1, 2, 4, 8
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -40,6 +41,10 @@ SIGNATURES = {
     "hca_compress": (_i32, [_p, _p, _p, _p, _p, _i32, _p, _p, _p, _i64, _i32, _i32, _p, _i32, _p, _f, _p, _p]),
     "rmsnorm_heads": (_i32, [_p, _i32, _i64, _i32, _p, _f, _p, _p]),
     "kv_quantize_fp8": (_i32, [_p, _i32, _i64, _p, _p]),
+    "mxfp4_quantize": (_i32, [_p, _i32, _i64, _i64, _p, _p, _p]),
+    "mxfp4_dequantize": (_i32, [_p, _p, _i64, _i64, _i32, _p, _p]),
+    "kv_quantize_fp4": (_i32, [_p, _i32, _i64, _p, _i64, _p, _p, _p]),
+    "kv_dequantize_fp4": (_i32, [_p, _p, _i64, _i64, _i32, _p, _p, _p]),
     "lindex_pool_keys": (_i32, [_p, _i32, _i32, _p, _p, _i32, _p, _p, _p, _i64, _p, _p, _p, _p]),
     "lindex_score_topk": (_i32, [_p, _p, _p, _p, _p, _p, _p, _p, _i32, _i32, _i32, _i32, _i32, _i32, _i64,
                                  _p, _p, _p, _i64, _p, _sz, _p, _p]),

@@ -13,7 +13,7 @@ import math
 import torch
 
 from . import _lib
-from ._lib import ATTN_KV_FP8, ATTN_PAIRS, BF16, CSA, F32, FP8E4M3, HCA, KV8_ROW_BYTES, OVERLAP_PREVIOUS  # noqa: F401
+from ._lib import ATTN_KV_FP8, ATTN_PAIRS, BF16, CSA, F32, FP8E4M3, HCA, KV4_ROW_BYTES, KV8_ROW_BYTES, OVERLAP_PREVIOUS  # noqa: F401
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16, torch.uint8: FP8E4M3, torch.float8_e4m3fn: FP8E4M3}
 
@@ -31,6 +31,27 @@ def _dt(t) -> int:
         return _DT[t.dtype]
     except KeyError:
         raise ValueError(f"unsupported dtype {t.dtype}") from None
+
+
+def _check(fn: str, **tensors) -> None:
+    """Device and layout of the tensors handed to `fn` (None: not given): name=(tensor, dtypes,
+    shape), dtypes a dtype or a tuple of them, shape a tuple with None for a free extent.  All of
+    them have to be contiguous and on the current CUDA device, whose stream the call runs on."""
+    dev = torch.cuda.current_device()
+    for name, (t, dts, shape) in tensors.items():
+        if t is None:
+            continue
+        if t.device.type != "cuda" or t.device.index != dev:
+            raise ValueError(f"{fn}: {name} is on {t.device}, not on the current device cuda:{dev}")
+        if t.dtype not in (dts if isinstance(dts, tuple) else (dts,)):
+            raise ValueError(f"{fn}: {name} has dtype {t.dtype}")
+        if len(t.shape) != len(shape) or any(s is not None and s != g for s, g in zip(shape, t.shape)):
+            raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} is not contiguous")
+
+
+_VALUES = (torch.float32, torch.bfloat16)
 
 
 def _stream(stream) -> int:
@@ -209,6 +230,69 @@ def kv_quantize_fp8(rows, out=None, stream=None):
     lib = _lib.load()
     st = lib.kv_quantize_fp8(_ptr(rows), _dt(rows), n, _ptr(out), _stream(stream))
     _lib.check("kv_quantize_fp8", st)
+    return out
+
+
+def mxfp4_quantize(x, codes=None, bscale=None, *, stream=None):
+    """MXFP4 form of x [..., D] (fp32 or bf16, D a multiple of 32): (codes [..., D/2] uint8, two
+    E2M1 codes a byte, bscale [..., D/32] uint8, one E8M0 scale per 32 values)."""
+    lead, D = tuple(x.shape[:-1]), int(x.shape[-1])
+    if D < 1 or D % 32:
+        raise ValueError(f"mxfp4_quantize: rows of {D} values; MXFP4 takes a multiple of 32")
+    if codes is None:
+        codes = torch.empty(*lead, D // 2, dtype=torch.uint8, device=x.device)
+    if bscale is None:
+        bscale = torch.empty(*lead, D // 32, dtype=torch.uint8, device=x.device)
+    _check("mxfp4_quantize", x=(x, _VALUES, lead + (D,)), codes=(codes, torch.uint8, lead + (D // 2,)),
+           bscale=(bscale, torch.uint8, lead + (D // 32,)))
+    st = _lib.load().mxfp4_quantize(_ptr(x), _dt(x), x.numel() // D, D, _ptr(codes), _ptr(bscale), _stream(stream))
+    _lib.check("mxfp4_quantize", st)
+    return codes, bscale
+
+
+def mxfp4_dequantize(codes, bscale, out=None, *, dtype=torch.bfloat16, stream=None):
+    """The values [..., D] of MXFP4 codes [..., D/2] with scales [..., D/32], as `dtype` (or out's)."""
+    lead, D = tuple(codes.shape[:-1]), 2 * int(codes.shape[-1])
+    if D < 1 or D % 32:
+        raise ValueError(f"mxfp4_dequantize: rows of {D} values; MXFP4 takes a multiple of 32")
+    if out is None:
+        out = torch.empty(*lead, D, dtype=dtype, device=codes.device)
+    _check("mxfp4_dequantize", codes=(codes, torch.uint8, lead + (D // 2,)),
+           bscale=(bscale, torch.uint8, lead + (D // 32,)), out=(out, _VALUES, lead + (D,)))
+    st = _lib.load().mxfp4_dequantize(_ptr(codes), _ptr(bscale), out.numel() // D, D, _dt(out), _ptr(out),
+                                      _stream(stream))
+    _lib.check("mxfp4_dequantize", st)
+    return out
+
+
+def kv_quantize_fp4(rows, out=None, *, dst=None, dev_status=None, stream=None):
+    """4-bit main-KV rows ([cap, 176] uint8) from K||V rows [n, 256] (fp32 or bf16).  dst [n]
+    int64: row i goes to out[dst[i]] (negative: left out; no two equal); None: to out[i].  Rows of
+    `out` that are not named stay as they were."""
+    n = int(rows.shape[0])
+    if out is None:
+        if dst is not None:
+            raise ValueError("kv_quantize_fp4: dst needs the cache it points into (out)")
+        out = torch.empty(n, KV4_ROW_BYTES, dtype=torch.uint8, device=rows.device)
+    _check("kv_quantize_fp4", rows=(rows, _VALUES, (n, 256)), out=(out, torch.uint8, (None, KV4_ROW_BYTES)),
+           dst=(dst, torch.int64, (n,)), dev_status=(dev_status, torch.int32, (1,)))
+    st = _lib.load().kv_quantize_fp4(_ptr(rows), _dt(rows), n, _ptr(dst), int(out.shape[0]), _ptr(out),
+                                     _ptr(dev_status), _stream(stream))
+    _lib.check("kv_quantize_fp4", st)
+    return out
+
+
+def kv_dequantize_fp4(cache, out=None, *, src=None, dtype=torch.bfloat16, dev_status=None, stream=None):
+    """K||V values [n, 256] (`dtype`, or out's) of the 4-bit main-KV rows cache [cap, 176]: rows
+    src [n] int64 of it (negative: zeros), or its first rows (all of them without `out`)."""
+    n = int(src.shape[0]) if src is not None else int(out.shape[0] if out is not None else cache.shape[0])
+    if out is None:
+        out = torch.empty(n, 256, dtype=dtype, device=cache.device)
+    _check("kv_dequantize_fp4", cache=(cache, torch.uint8, (None, KV4_ROW_BYTES)), out=(out, _VALUES, (n, 256)),
+           src=(src, torch.int64, (n,)), dev_status=(dev_status, torch.int32, (1,)))
+    st = _lib.load().kv_dequantize_fp4(_ptr(cache), _ptr(src), int(cache.shape[0]), n, _dt(out), _ptr(out),
+                                       _ptr(dev_status), _stream(stream))
+    _lib.check("kv_dequantize_fp4", st)
     return out
 
 

@@ -191,6 +191,61 @@ int kv_quantize_fp8(const void* rows, int dtype, int64_t n, void* out, cskv_stre
   return launch_status(cskv::launch_kv_quantize_fp8(rows, dtype, n, (uint8_t*)out, (cudaStream_t)stream));
 }
 
+// Value dtypes of the quantisers: CSKV_F32 or CSKV_BF16.
+static int check_value_dtype(int dtype) {
+  if (dtype == CSKV_F32 || dtype == CSKV_BF16) return CSKV_OK;
+  return dtype == CSKV_FP8E4M3 ? CSKV_ERR_UNSUPPORTED : CSKV_ERR_INVALID_ARG;
+}
+
+// Shape and pointers of mxfp4_quantize / mxfp4_dequantize; 2^44 values bound the grid.
+static int check_mxfp4(const void* x, int dtype, int64_t rows, int64_t D, const uint8_t* codes,
+                       const uint8_t* bscale) {
+  if (rows < 0 || D < 1 || D % 32 || D > (1LL << 44) || rows > (1LL << 44) / D) return CSKV_ERR_INVALID_ARG;
+  const int rc = check_value_dtype(dtype);
+  if (rc || rows == 0) return rc;
+  if (!x || !codes || !bscale || !aligned16(x) || !aligned16(codes)) return CSKV_ERR_INVALID_ARG;
+  return CSKV_OK;
+}
+
+int mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t D, uint8_t* codes, uint8_t* bscale,
+                   cskv_stream_t stream) {
+  const int rc = check_mxfp4(x, dtype, rows, D, codes, bscale);
+  if (rc || rows == 0) return rc;
+  return launch_status(launch_mxfp4_quantize(x, dtype, rows * (D / 32), codes, bscale, (cudaStream_t)stream));
+}
+
+int mxfp4_dequantize(const uint8_t* codes, const uint8_t* bscale, int64_t rows, int64_t D, int dtype, void* out,
+                     cskv_stream_t stream) {
+  const int rc = check_mxfp4(out, dtype, rows, D, codes, bscale);
+  if (rc || rows == 0) return rc;
+  return launch_status(launch_mxfp4_dequantize(codes, bscale, rows * (D / 32), dtype, out, (cudaStream_t)stream));
+}
+
+// Sizes and pointers of kv_quantize_fp4 / kv_dequantize_fp4; 2^35 rows bound the grid.
+static int check_kv4(const void* rows, int dtype, int64_t n, const int64_t* list, int64_t cap, const void* cache) {
+  if (n < 0 || n > (1LL << 35) || cap < 0 || (!list && cap < n)) return CSKV_ERR_INVALID_ARG;
+  const int rc = check_value_dtype(dtype);
+  if (rc || n == 0) return rc;
+  if (!rows || !cache || !aligned16(rows) || !aligned16(cache)) return CSKV_ERR_INVALID_ARG;
+  return reinterpret_cast<uintptr_t>(list) & 7u ? CSKV_ERR_INVALID_ARG : CSKV_OK;
+}
+
+int kv_quantize_fp4(const void* rows, int dtype, int64_t n, const int64_t* dst, int64_t cap, void* out,
+                    int* dev_status, cskv_stream_t stream) {
+  const int rc = check_kv4(rows, dtype, n, dst, cap, out);
+  if (rc || n == 0) return rc;
+  return launch_status(
+      launch_kv_quantize_fp4(rows, dtype, n, dst, cap, (uint8_t*)out, dev_status, (cudaStream_t)stream));
+}
+
+int kv_dequantize_fp4(const void* cache, const int64_t* src, int64_t cap, int64_t n, int dtype, void* out,
+                      int* dev_status, cskv_stream_t stream) {
+  const int rc = check_kv4(out, dtype, n, src, cap, cache);
+  if (rc || n == 0) return rc;
+  return launch_status(launch_kv_dequantize_fp4((const uint8_t*)cache, src, cap, n, dtype, out, dev_status,
+                                                (cudaStream_t)stream));
+}
+
 int rmsnorm_heads(const void* x, int dtype, int64_t rows, int d, const float* gamma, float eps, void* out,
                   cskv_stream_t stream) {
   if (dtype != CSKV_F32 && dtype != CSKV_BF16) return dtype == CSKV_FP8E4M3 ? CSKV_ERR_UNSUPPORTED : CSKV_ERR_INVALID_ARG;

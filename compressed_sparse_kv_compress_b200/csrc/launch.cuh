@@ -159,6 +159,15 @@ int check_attn_args(int mode, const void* q, const void* kv_cmp, const int64_t* 
                     const float* out);
 // kv8.cu
 cudaError_t launch_kv_quantize_fp8(const void* rows, int dtype, int64_t n, uint8_t* out, cudaStream_t stream);
+// mx4.cu
+cudaError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t blocks, uint8_t* codes, uint8_t* scales,
+                                  cudaStream_t stream);
+cudaError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t blocks, int dtype, void* out,
+                                    cudaStream_t stream);
+cudaError_t launch_kv_quantize_fp4(const void* rows, int dtype, int64_t n, const int64_t* dst, int64_t cap,
+                                   uint8_t* out, int* st, cudaStream_t stream);
+cudaError_t launch_kv_dequantize_fp4(const uint8_t* cache, const int64_t* src, int64_t cap, int64_t n, int dtype,
+                                     void* out, int* st, cudaStream_t stream);
 // staging.cu
 cudaError_t launch_copy_segments(const void* src, const int64_t* src_off, void* const* dst, const int64_t* len, int n,
                                  cudaStream_t stream);

@@ -1,0 +1,214 @@
+// Quantisers of MXFP4 vectors and of 4-bit main-KV rows, and their inverses (formats in mx4.cuh;
+// [SW] shareware.cn/news/167317 §六.1, §十三.4).
+//
+// All four stream memory: a value is read once and its code written once.  A lane takes eight
+// neighbouring values (16 or 32 bytes a load), so four lanes hold a block: its largest magnitude
+// is two shuffles (compared as integers: the order of non-negative floats, and an infinity or a
+// NaN stays the largest), and a warp's loads and code stores are contiguous.
+#include "launch.cuh"
+#include "mx4.cuh"
+
+namespace cskv {
+
+constexpr int kMxThreads = 256;
+constexpr int kMxUnroll = 4;                          // 256-value pieces of a warp in flight
+constexpr int kMxWarpValues = 256 * kMxUnroll;        // values a warp takes
+constexpr int kMxCtaValues = kMxWarpValues * (kMxThreads / 32);
+
+// Largest magnitude (as bits) of the four lanes that hold a block.
+__device__ __forceinline__ uint32_t block_amax(const float (&x)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+
+// x * 2^(127 - e) for the conversion; in a block without a finite scale every code is zero.
+__device__ __forceinline__ void scale_down(float (&x)[8], uint32_t e) {
+  const float inv = mx_inv_scale(e);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = e == 0xFFu ? 0.f : x[i] * inv;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kMxThreads) mxfp4_quantize_kernel(const T* __restrict__ x, int64_t blocks,
+                                                                    uint8_t* __restrict__ codes,
+                                                                    uint8_t* __restrict__ scales) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  // first block of this warp; a lane's piece u is block b0 + 8u + lane/4, values 8 (lane % 4) ..
+  const int64_t b0 = ((int64_t)blockIdx.x * kMxCtaValues + (threadIdx.x >> 5) * kMxWarpValues) / kMxBlock;
+  float f[kMxUnroll][8];
+#pragma unroll
+  for (int u = 0; u < kMxUnroll; ++u) {
+    if (b0 + 8 * u + (lane >> 2) < blocks)
+      Vec8<T>::load(x + b0 * kMxBlock + 256 * u + 8 * lane, f[u]);
+    else
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[u][i] = 0.f;
+  }
+  uint32_t mine = 0;
+#pragma unroll
+  for (int u = 0; u < kMxUnroll; ++u) {
+    const uint32_t e = mx_scale_code(block_amax(f[u]), kE2m1Emax);
+    scale_down(f[u], e);
+    if ((lane & 3) == u) mine = e;
+    if (b0 + 8 * u + (lane >> 2) < blocks)
+      *reinterpret_cast<uint32_t*>(codes + (b0 * kMxBlock + 256 * u + 8 * lane) / 2) = e2m1x8(f[u]);
+  }
+  // lane l keeps the scale of piece l % 4, block l / 4: a warp's 32 scale bytes in one store
+  const int64_t b = b0 + 8 * (lane & 3) + (lane >> 2);
+  if (b < blocks) scales[b] = (uint8_t)mine;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kMxThreads) mxfp4_dequantize_kernel(const uint8_t* __restrict__ codes,
+                                                                      const uint8_t* __restrict__ scales,
+                                                                      int64_t blocks, T* __restrict__ out) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t b0 = ((int64_t)blockIdx.x * kMxCtaValues + (threadIdx.x >> 5) * kMxWarpValues) / kMxBlock;
+  uint32_t w[kMxUnroll];
+  float s[kMxUnroll];
+#pragma unroll
+  for (int u = 0; u < kMxUnroll; ++u) {
+    const int64_t b = b0 + 8 * u + (lane >> 2);
+    const bool ok = b < blocks;
+    w[u] = ok ? __ldg(reinterpret_cast<const uint32_t*>(codes + (b0 * kMxBlock + 256 * u + 8 * lane) / 2)) : 0u;
+    s[u] = ok ? mx_scale(__ldg(scales + b)) : 0.f;
+  }
+#pragma unroll
+  for (int u = 0; u < kMxUnroll; ++u) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = e2m1_value(w[u] >> (4 * i)) * s[u];
+    if (b0 + 8 * u + (lane >> 2) < blocks) Vec8<T>::store(out + b0 * kMxBlock + 256 * u + 8 * lane, f);
+  }
+}
+
+// ---------------------------------------------------------------- 4-bit main-KV rows
+// A warp a row, a lane eight of its 256 values: lanes 0..7 and 16..31 hold E2M1 dims, 8..15 the
+// E4M3 RoPE dims.
+constexpr int kKv4Warps = 8;
+constexpr int kKv4Rows = 4;  // rows of a warp in flight
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kKv4Warps) kv_quantize_fp4_kernel(const T* __restrict__ rows, int64_t n,
+                                                                        const int64_t* __restrict__ dst, int64_t cap,
+                                                                        uint8_t* __restrict__ out, int* st) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t r0 = ((int64_t)blockIdx.x * kKv4Warps + (threadIdx.x >> 5)) * kKv4Rows;
+  const bool rope = lane >= 8 && lane < 16;
+  float x[kKv4Rows][8];
+  int64_t to[kKv4Rows];
+#pragma unroll
+  for (int u = 0; u < kKv4Rows; ++u) {
+    const int64_t r = r0 + u;
+    to[u] = r >= n ? -1 : dst ? __ldg(dst + r) : r;
+    if (r < n)
+      Vec8<T>::load(rows + (size_t)r * kRow + 8 * lane, x[u]);
+    else
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+  }
+#pragma unroll
+  for (int u = 0; u < kKv4Rows; ++u) {
+    const uint32_t e = mx_scale_code(block_amax(x[u]), rope ? kE4m3Emax : kE2m1Emax);
+    scale_down(x[u], e);
+    // the eight scale bytes sit in lanes 0, 4, .. 28; lane 0 collects them
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      lo |= __shfl_sync(0xffffffffu, e, 4 * b) << (8 * b);
+      hi |= __shfl_sync(0xffffffffu, e, 16 + 4 * b) << (8 * b);
+    }
+    if (to[u] < 0) continue;
+    if (to[u] >= cap) {
+      if (lane == 0) flag(st, CSKV_DEV_BAD_INDEX);
+      continue;
+    }
+    uint8_t* o = out + (size_t)to[u] * kKv4RowBytes;
+    if (rope)
+      *reinterpret_cast<uint2*>(o + kKv4Rope + 8 * (lane - 8)) = e4m3x8(x[u]);
+    else
+      *reinterpret_cast<uint32_t*>(o + (lane < 8 ? 4 * lane : kKv4V + 4 * (lane - 16))) = e2m1x8(x[u]);
+    if (lane == 0) *reinterpret_cast<uint4*>(o + kKv4Scales) = make_uint4(lo, hi, 0u, 0u);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kKv4Warps) kv_dequantize_fp4_kernel(const uint8_t* __restrict__ cache,
+                                                                          const int64_t* __restrict__ src,
+                                                                          int64_t cap, int64_t n,
+                                                                          T* __restrict__ out, int* st) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t r0 = ((int64_t)blockIdx.x * kKv4Warps + (threadIdx.x >> 5)) * kKv4Rows;
+  float x[kKv4Rows][8];
+#pragma unroll
+  for (int u = 0; u < kKv4Rows; ++u) {
+    const int64_t r = r0 + u;
+    int64_t e = r >= n ? -1 : src ? __ldg(src + r) : r;
+    if (e >= cap) {
+      if (lane == 0) flag(st, CSKV_DEV_BAD_INDEX);
+      e = -1;
+    }
+    if (e >= 0)
+      kv4_load8(cache + (size_t)e * kKv4RowBytes, lane, x[u]);
+    else
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+  }
+#pragma unroll
+  for (int u = 0; u < kKv4Rows; ++u)
+    if (r0 + u < n) Vec8<T>::store(out + (size_t)(r0 + u) * kRow + 8 * lane, x[u]);
+}
+
+// ---------------------------------------------------------------- launchers
+template <typename... KArgs, typename... Args>
+static cudaError_t launch_1d(void (*kern)(KArgs...), int64_t ctas, int threads, cudaStream_t stream, Args... args) {
+  cudaError_t e = ensure_smem(kern, 0);
+  if (e == cudaSuccess) e = launch_dependent(kern, dim3((unsigned)ctas), dim3(threads), 0, stream, args...);
+  note_launch();
+  return e;
+}
+
+cudaError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t blocks, uint8_t* codes, uint8_t* scales,
+                                  cudaStream_t stream) {
+  const int64_t ctas = (blocks * kMxBlock + kMxCtaValues - 1) / kMxCtaValues;
+  return dtype == CSKV_F32
+             ? launch_1d(mxfp4_quantize_kernel<float>, ctas, kMxThreads, stream, (const float*)x, blocks, codes, scales)
+             : launch_1d(mxfp4_quantize_kernel<__nv_bfloat16>, ctas, kMxThreads, stream, (const __nv_bfloat16*)x,
+                         blocks, codes, scales);
+}
+
+cudaError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t blocks, int dtype, void* out,
+                                    cudaStream_t stream) {
+  const int64_t ctas = (blocks * kMxBlock + kMxCtaValues - 1) / kMxCtaValues;
+  return dtype == CSKV_F32
+             ? launch_1d(mxfp4_dequantize_kernel<float>, ctas, kMxThreads, stream, codes, scales, blocks, (float*)out)
+             : launch_1d(mxfp4_dequantize_kernel<__nv_bfloat16>, ctas, kMxThreads, stream, codes, scales, blocks,
+                         (__nv_bfloat16*)out);
+}
+
+cudaError_t launch_kv_quantize_fp4(const void* rows, int dtype, int64_t n, const int64_t* dst, int64_t cap,
+                                   uint8_t* out, int* st, cudaStream_t stream) {
+  const int64_t ctas = (n + kKv4Warps * kKv4Rows - 1) / (kKv4Warps * kKv4Rows);
+  return dtype == CSKV_F32 ? launch_1d(kv_quantize_fp4_kernel<float>, ctas, 32 * kKv4Warps, stream, (const float*)rows,
+                                       n, dst, cap, out, st)
+                           : launch_1d(kv_quantize_fp4_kernel<__nv_bfloat16>, ctas, 32 * kKv4Warps, stream,
+                                       (const __nv_bfloat16*)rows, n, dst, cap, out, st);
+}
+
+cudaError_t launch_kv_dequantize_fp4(const uint8_t* cache, const int64_t* src, int64_t cap, int64_t n, int dtype,
+                                     void* out, int* st, cudaStream_t stream) {
+  const int64_t ctas = (n + kKv4Warps * kKv4Rows - 1) / (kKv4Warps * kKv4Rows);
+  return dtype == CSKV_F32 ? launch_1d(kv_dequantize_fp4_kernel<float>, ctas, 32 * kKv4Warps, stream, cache, src, cap,
+                                       n, (float*)out, st)
+                           : launch_1d(kv_dequantize_fp4_kernel<__nv_bfloat16>, ctas, 32 * kKv4Warps, stream, cache,
+                                       src, cap, n, (__nv_bfloat16*)out, st);
+}
+
+}  // namespace cskv

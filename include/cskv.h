@@ -60,6 +60,7 @@ enum cskv_mode { CSKV_CSA = 0, CSKV_HCA = 1 };
 #define CSKV_ATTN_PAIRS 0x100
 #define CSKV_ATTN_KV_FP8 0x200  /* hybrid_decode_attn: kv_cmp rows are FP8 main-KV rows */
 #define CSKV_KV8_ROW_BYTES 336  /* bytes of one FP8 main-KV row (kv_quantize_fp8) */
+#define CSKV_KV4_ROW_BYTES 176  /* bytes of one 4-bit main-KV row (kv_quantize_fp4) */
 
 /* Bits OR-ed into *dev_status by device-side checks. */
 enum cskv_dev_status {
@@ -175,6 +176,57 @@ CSKV_API int hca_compress(const void* x, const void* z, const float* bias,
  * with n > 0, n < 0 or n > 8 (2^31 - 1), bad dtype), CSKV_ERR_UNSUPPORTED (FP8 input).
  * ------------------------------------------------------------------------ */
 CSKV_API int kv_quantize_fp8(const void* rows, int dtype, int64_t n, void* out, cskv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * mxfp4_quantize / mxfp4_dequantize -- MXFP4 vectors from rows of values, and back.
+ *
+ * [SW] §六.1 / §十三.4, [TR] §4.2: the indexer's QK path may run in FP4.  Every 32
+ * neighbouring values of a row share one E8M0 scale 2^(e - 127); the values are OCP E2M1
+ * codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two per byte, element 2j in the low
+ * nibble of byte j.  The shared exponent is floor(log2(amax)) - 2, at least -127 (a block of
+ * zeros: e = 0); code = E2M1(value / scale), round to nearest even, saturating.  A block
+ * that holds an infinity or a NaN gets e = 0xFF (NaN) and zero codes.  The division is exact,
+ * so the codes are those of exact arithmetic.  These are the arrays that
+ * lindex_score_topk_mxfp4 and mxfp4_matmul read.
+ * x / out  : [rows, D] dtype (CSKV_F32 or CSKV_BF16), 16-byte aligned.
+ * codes    : [rows, D/2] uint8, 16-byte aligned;  bscale: [rows, D/32] uint8.
+ * D        : a positive multiple of 32.
+ * mxfp4_dequantize writes code x scale, rounded to dtype (exact but for bf16's range).
+ * rows == 0 launches nothing.  Errors: CSKV_ERR_INVALID_ARG (null or misaligned pointer with
+ * rows > 0, rows < 0, bad D or dtype, more than 2^44 values), CSKV_ERR_UNSUPPORTED (FP8).
+ * ------------------------------------------------------------------------ */
+CSKV_API int mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t D, uint8_t* codes, uint8_t* bscale,
+                 cskv_stream_t stream);
+CSKV_API int mxfp4_dequantize(const uint8_t* codes, const uint8_t* bscale, int64_t rows, int64_t D, int dtype,
+                 void* out, cskv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * kv_quantize_fp4 / kv_dequantize_fp4 -- 4-bit main-KV rows from K||V rows, and back.
+ *
+ * [SW] §十三.4: the main KV may be stored in few bits while the dimensions most sensitive to
+ * position information keep a higher precision.  A compressed row (K dims 0..127 then V dims
+ * 0..127) becomes CSKV_KV4_ROW_BYTES (176) bytes: K dims 0..63 as E2M1 codes (32 B) | K dims
+ * 64..127, the RoPE dims, as E4M3 codes (64 B) | V dims 0..127 as E2M1 codes (64 B) | one E8M0
+ * scale for each 32 of the 256 values (8 B) | 8 zero bytes.  Scales and codes as
+ * mxfp4_quantize; an E4M3 block's shared exponent is floor(log2(amax)) - 8 and its codes
+ * saturate at 448 (the quantiser writes no NaN code; 0x7F and 0xFF would read as +-480).
+ * hybrid_decode_attn reads such rows with CSKV_ATTN_KV_FP4.
+ * rows / out (values) : [n, 256] dtype (CSKV_F32 or CSKV_BF16), 16-byte aligned.
+ * out (quantise) / cache (dequantise) : [cap, 176] bytes, 16-byte aligned.
+ * dst  : [n] int64 or NULL: row i goes to cache row dst[i] (NULL: i, and n <= cap).  Rows with
+ *        dst < 0 are left out; dst >= cap is flagged CSKV_DEV_BAD_INDEX and left out.  Cache
+ *        rows that no dst names stay as they were.  No two dst may be equal.
+ * src  : [n] int64 or NULL: value row i comes from cache row src[i] (NULL: i, and n <= cap).
+ *        A negative src gives a row of zeros; src >= cap is flagged CSKV_DEV_BAD_INDEX and
+ *        gives zeros.  A source row may be named any number of times.
+ * n == 0 launches nothing.  Errors: CSKV_ERR_INVALID_ARG (null or misaligned pointer with
+ * n > 0, n < 0 or n > 2^35, cap < 0, cap < n without a list, bad dtype), CSKV_ERR_UNSUPPORTED
+ * (FP8).
+ * ------------------------------------------------------------------------ */
+CSKV_API int kv_quantize_fp4(const void* rows, int dtype, int64_t n, const int64_t* dst, int64_t cap, void* out,
+                 int* dev_status, cskv_stream_t stream);
+CSKV_API int kv_dequantize_fp4(const void* cache, const int64_t* src, int64_t cap, int64_t n, int dtype, void* out,
+                 int* dev_status, cskv_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * rmsnorm_heads -- RMSNorm of head vectors (the query-side pass).
