@@ -13,7 +13,7 @@ import math
 import torch
 
 from . import _lib
-from ._lib import ATTN_KV_FP8, ATTN_PAIRS, BF16, CSA, F32, FP8E4M3, HCA, KV4_ROW_BYTES, KV8_ROW_BYTES, OVERLAP_PREVIOUS  # noqa: F401
+from ._lib import ATTN_KV_FP4, ATTN_KV_FP8, ATTN_OUT_BF16, ATTN_PAIRS, BF16, CSA, F32, FP8E4M3, HCA, KV4_ROW_BYTES, KV8_ROW_BYTES, OVERLAP_PREVIOUS  # noqa: F401
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16, torch.uint8: FP8E4M3, torch.float8_e4m3fn: FP8E4M3}
 
@@ -187,15 +187,23 @@ def attn_workspace(mode, T, H, k, window, max_entries, device="cuda") -> torch.T
 
 def hybrid_decode_attn(mode, q, kv_cmp, cmp_off, kv_raw, raw_off, q_seq, q_pos, out, workspace, *, window,
                        idx=None, raw_tok0=None, sink=None, scale=None, lse=None, max_entries=0, adjacent_pairs=False,
-                       kv_fp8=False, dev_status=None, stream=None):
+                       kv_fp8=False, kv_fp4=False, dev_status=None, stream=None):
     """adjacent_pairs: CSKV_ATTN_PAIRS (queries 2j, 2j + 1 are one sequence's consecutive
     positions; see the C header).  kv_fp8: CSKV_ATTN_KV_FP8, kv_cmp holds FP8 main-KV rows
-    ([entries, 336] uint8, from kv_quantize_fp8)."""
+    ([entries, 336] uint8, from kv_quantize_fp8).  kv_fp4: CSKV_ATTN_KV_FP4, kv_cmp holds 4-bit
+    main-KV rows ([entries, 176] uint8, from kv_quantize_fp4).  out is [T, H, 128] fp32, or bf16
+    (CSKV_ATTN_OUT_BF16)."""
     T, H, d = q.shape
     if adjacent_pairs:
         mode = int(mode) | ATTN_PAIRS
     if kv_fp8:
         mode = int(mode) | ATTN_KV_FP8
+    if kv_fp4:
+        mode = int(mode) | ATTN_KV_FP4
+        _check("hybrid_decode_attn", q=(q, _VALUES, (T, H, d)), kv_cmp=(kv_cmp, torch.uint8, (None, KV4_ROW_BYTES)),
+               kv_raw=(kv_raw, q.dtype, (None, 256)), out=(out, _VALUES, (T, H, d)))
+    if out.dtype == torch.bfloat16:
+        mode = int(mode) | ATTN_OUT_BF16
     k = idx.shape[1] if idx is not None else 0
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     lib = _lib.load()

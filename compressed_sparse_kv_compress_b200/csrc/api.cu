@@ -457,7 +457,7 @@ static int attn_plan(int mode, int T, int k, int window, int64_t max_entries, bo
 constexpr int kPairHeads = 64;
 
 size_t hybrid_attn_workspace_size(int mode, int T, int H, int d, int k, int window, int64_t max_entries) {
-  mode &= ~(CSKV_ATTN_PAIRS | CSKV_ATTN_KV_FP8);
+  mode &= ~kAttnFlags;
   if (T < 1 || H < 1 || d != kHeadDim || window < 0) return 0;
   size_t best = 0;
   for (int tc = 0; tc < 2; ++tc) {
@@ -484,9 +484,10 @@ int cskv::check_attn_args(int mode, const void* q, const void* kv_cmp, const int
                           int k, const void* kv_raw, const int64_t* raw_off, int window, float scale,
                           const int32_t* q_seq, const int64_t* q_pos, int batch, int T, int H, int d, int dtype,
                           int64_t max_entries, const float* out) {
-  constexpr int kFlags = CSKV_ATTN_PAIRS | CSKV_ATTN_KV_FP8;
-  if ((mode & ~kFlags) != CSKV_CSA && (mode & ~kFlags) != CSKV_HCA) return CSKV_ERR_INVALID_ARG;
-  mode &= ~kFlags;
+  if ((mode & ~kAttnFlags) != CSKV_CSA && (mode & ~kAttnFlags) != CSKV_HCA) return CSKV_ERR_INVALID_ARG;
+  if ((mode & CSKV_ATTN_KV_FP8) && (mode & CSKV_ATTN_KV_FP4)) return CSKV_ERR_INVALID_ARG;
+  const bool out_bf16 = (mode & CSKV_ATTN_OUT_BF16) != 0, kv4 = (mode & CSKV_ATTN_KV_FP4) != 0;
+  mode &= ~kAttnFlags;
   if (dtype != CSKV_F32 && dtype != CSKV_BF16) return dtype == CSKV_FP8E4M3 ? CSKV_ERR_UNSUPPORTED : CSKV_ERR_INVALID_ARG;
   if (d != kHeadDim) return CSKV_ERR_UNSUPPORTED;
   if (H < 1 || H > 128 || T < 0 || window < 0 || window > (1 << 20) || batch < 1) return CSKV_ERR_INVALID_ARG;
@@ -498,6 +499,8 @@ int cskv::check_attn_args(int mode, const void* q, const void* kv_cmp, const int
   if (T == 0) return CSKV_OK;
   if (!q || !kv_cmp || !cmp_off || !kv_raw || !raw_off || !q_seq || !q_pos || !out) return CSKV_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(kv_cmp) || !aligned16(kv_raw)) return CSKV_ERR_INVALID_ARG;
+  // outputs that are stored in wide words
+  if ((out_bf16 || kv4) && !aligned16(out)) return CSKV_ERR_INVALID_ARG;
   return CSKV_OK;
 }
 
@@ -513,15 +516,26 @@ int hybrid_decode_attn(int mode, const void* q, const void* kv_cmp, const int64_
   if (arc != CSKV_OK || T == 0) return arc;
   const bool want_pairs = (mode & CSKV_ATTN_PAIRS) != 0;
   const bool kv8 = (mode & CSKV_ATTN_KV_FP8) != 0;  // FP8 main-KV rows, decoded as gathered
-  mode &= ~(CSKV_ATTN_PAIRS | CSKV_ATTN_KV_FP8);
+  const bool kv4 = (mode & CSKV_ATTN_KV_FP4) != 0;  // 4-bit main-KV rows, decoded as gathered
+  const bool out_bf16 = (mode & CSKV_ATTN_OUT_BF16) != 0;
+  mode &= ~kAttnFlags;
   const bool tc = dtype == CSKV_BF16;
   AttnPlan pl;
   int rc = attn_plan(mode, T, mode == CSKV_CSA ? k : 0, window, max_entries, tc, &pl);
   if (rc) return rc;
+  int sms = 0;
+  if (tc && kv4) {
+    // the 4-bit kernel's own plan, inside the workspace that the call without the flag would need
+    rc = device_sms(&sms);
+    if (rc) return rc;
+    pl.cluster = 0;
+    attn_kv4_plan(T, (mode == CSKV_CSA ? (int64_t)k : max_entries) + window, pl.ws_splits, sms, &pl.R, &pl.S);
+    pl.ws_splits = pl.S;
+  }
   // adjacent-query pairs: the HCA tensor-core kernel with 64 heads, when the pairs' plan merges
   // inside a cluster (a unit of two queries is one 128-head "query" of the plan)
   int units = T, Hv = H;
-  if (want_pairs && tc && mode == CSKV_HCA && H == kPairHeads && T >= 2) {
+  if (want_pairs && tc && !kv4 && mode == CSKV_HCA && H == kPairHeads && T >= 2) {
     AttnPlan pp;
     rc = attn_plan(mode, (T + 1) / 2, 0, window + 1, max_entries, tc, &pp);
     if (rc) return rc;
@@ -557,11 +571,14 @@ int hybrid_decode_attn(int mode, const void* q, const void* kv_cmp, const int64_
   p.pairs = Hv != H ? 1 : 0;
   p.Hv = Hv;
   p.kv8 = kv8 ? 1 : 0;
+  p.kv4 = kv4 ? 1 : 0;
+  p.out_bf16 = out_bf16 ? 1 : 0;
   p.part_acc = (float*)workspace;
   p.part_ml = p.part_acc + (size_t)units * pl.S * Hv * kHeadDim;
   p.out = out;
   p.lse = lse;
   p.st = dev_status;
+  if (tc && kv4) return launch_status(launch_attn_kv4(p, sms, (cudaStream_t)stream));
   if (tc) return launch_status(launch_attn_tc(p, (cudaStream_t)stream));
   return launch_status(launch_attn_generic(p, dtype, (cudaStream_t)stream));
 }

@@ -14,10 +14,11 @@
 // CTA (split s, query t) runs an online softmax over rows [s*R, (s+1)*R) in tiles of 32
 // and writes (m, l, acc) in the log2 domain; attn_combine merges the splits of a query
 // and folds the sink logit in once.  This generic kernel serves fp32 and any head count, and
-// FP8 main-KV rows (KV8: kv_cmp rows in the kv8.cuh layout, dequantised as they are loaded;
-// the window's raw rows stay bf16 / fp32); bf16 with many heads goes to the tensor-core kernel.
+// FP8 or 4-bit main-KV rows (KV = 8, 4: kv_cmp rows in the kv8.cuh or mx4.cuh layout, dequantised as
+// they are loaded; the window's raw rows stay bf16 / fp32); bf16 queries go to the tensor-core kernels.
 #include "attn_rows.cuh"
 #include "kv8.cuh"
+#include "mx4.cuh"
 
 namespace cskv {
 
@@ -26,7 +27,7 @@ constexpr int kAttnThreads = 256;
 constexpr int kAttnTile = 32;
 constexpr int kPsStride = kAttnTile + 1;  // padded row of the probability tile
 
-template <typename T, int HP, bool KV8>
+template <typename T, int HP, int KV>
 __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnParams p) {
   constexpr int d = kHeadDim;
   constexpr int TPH = kAttnThreads / HP;  // threads per head in the PV update
@@ -77,7 +78,9 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnParams p) 
       if (part == 0) valid[rr] = off >= 0;
       if (off >= 0) {
         float f[32];
-        if (KV8 && !is_raw) {
+        if (KV == 4 && !is_raw) {
+          kv4_load_part(reinterpret_cast<const uint8_t*>(p.kv_cmp) + (size_t)(off / kRow) * kKv4RowBytes, part, f);
+        } else if (KV == 8 && !is_raw) {
           kv8_load_part(reinterpret_cast<const uint8_t*>(p.kv_cmp) + (size_t)(off / kRow) * kKv8RowBytes, part, f);
         } else {
           const T* src = (is_raw ? raw : cmp) + off + part * 32;
@@ -174,6 +177,14 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnParams p) 
 // each group folds its splits under its own max; otherwise two passes with independent loads
 // (so many are in flight at once): the max over the splits' m, merged across groups in shared
 // memory, then the weighted sums of l and acc under that common max, summed across groups.
+// Element i of the output, in its dtype.
+__device__ __forceinline__ void store_out(const AttnParams& p, size_t i, float v) {
+  if (p.out_bf16)
+    reinterpret_cast<__nv_bfloat16*>(p.out)[i] = __float2bfloat16_rn(v);
+  else
+    p.out[i] = v;
+}
+
 constexpr int kCombineDims = 2;
 constexpr int kCombineGroups = 4;
 constexpr int kFewSplits = 5;  // splits per group folded in one round of loads
@@ -245,9 +256,9 @@ __global__ void __launch_bounds__(128 * kCombineGroups) attn_combine_kernel(Attn
       }
     }
     const float inv = Lt > 0.f ? 1.f / Lt : 0.f;
-    float* dst = p.out + ((size_t)t * H + h) * kHeadDim + j0;
+    const size_t dst = ((size_t)t * H + h) * kHeadDim + j0;
 #pragma unroll
-    for (int jj = 0; jj < kCombineDims; ++jj) dst[jj] = ot[jj] * inv;
+    for (int jj = 0; jj < kCombineDims; ++jj) store_out(p, dst + jj, ot[jj] * inv);
     if (j0 == 0 && p.lse) p.lse[(size_t)t * H + h] = Lt > 0.f ? (Mt + log2f(Lt)) * 0.69314718055994531f : -INFINITY;
     return;
   }
@@ -301,9 +312,9 @@ __global__ void __launch_bounds__(128 * kCombineGroups) attn_combine_kernel(Attn
     Lt = Ls * fp + (p.sink ? exp2f(sk - Mt) : 0.f);
   }
   const float inv = Lt > 0.f ? fp / Lt : 0.f;
-  float* dst = p.out + ((size_t)t * H + h) * kHeadDim + j0;
+  const size_t dst = ((size_t)t * H + h) * kHeadDim + j0;
 #pragma unroll
-  for (int jj = 0; jj < kCombineDims; ++jj) dst[jj] = os[jj] * inv;
+  for (int jj = 0; jj < kCombineDims; ++jj) store_out(p, dst + jj, os[jj] * inv);
   if (j0 == 0 && p.lse) p.lse[(size_t)t * H + h] = Lt > 0.f ? (Mt + log2f(Lt)) * 0.69314718055994531f : -INFINITY;
 }
 
@@ -354,10 +365,10 @@ int attn_max_splits(int mode, int k, int window, int64_t max_entries, int R) {
   return (int)(s > 0 ? s : 1);
 }
 
-template <typename T, int HP, bool KV8>
+template <typename T, int HP, int KV>
 static cudaError_t launch_split_as(const AttnParams& p, cudaStream_t stream) {
   const size_t smem = attn_smem(HP);
-  auto kern = attn_split_kernel<T, HP, KV8>;
+  auto kern = attn_split_kernel<T, HP, KV>;
   cudaError_t e = ensure_smem(kern, smem);
   if (e != cudaSuccess) return e;
   dim3 grid(p.max_splits, p.T);
@@ -368,7 +379,9 @@ static cudaError_t launch_split_as(const AttnParams& p, cudaStream_t stream) {
 
 template <typename T, int HP>
 static cudaError_t launch_split(const AttnParams& p, cudaStream_t stream) {
-  return p.kv8 ? launch_split_as<T, HP, true>(p, stream) : launch_split_as<T, HP, false>(p, stream);
+  return p.kv4 ? launch_split_as<T, HP, 4>(p, stream)
+         : p.kv8 ? launch_split_as<T, HP, 8>(p, stream)
+                 : launch_split_as<T, HP, 0>(p, stream);
 }
 
 cudaError_t launch_attn_generic(const AttnParams& p, int dtype, cudaStream_t stream) {

@@ -110,7 +110,8 @@ __device__ __forceinline__ void cluster_merge(const AttnParams& p, int t, float4
   const float inv = L > 0.f ? 1.f / L : 0.f;
   if (!mbar_wait_bounded(bar_m, 0)) flag(p.st, CSKV_DEV_TIMEOUT);
   if (!mine) return;
-  float* dst = p.out + ((size_t)t * H + h) * kHeadDim;
+  const size_t row = ((size_t)t * H + h) * kHeadDim;
+  float* dst = p.out + row;
 #pragma unroll
   for (int k = 0; k < NG; ++k) {
     const int g = g0 + CS * k;
@@ -124,6 +125,12 @@ __device__ __forceinline__ void cluster_merge(const AttnParams& p, int t, float4
         a.z = fmaf(v.z, f[s], a.z);
         a.w = fmaf(v.w, f[s], a.w);
       }
+    if (p.out_bf16) {
+      uint32_t* db = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(p.out) + row + 4 * g);
+      db[0] = pack_bf16(a.x * inv, a.y * inv);
+      db[1] = pack_bf16(a.z * inv, a.w * inv);
+      continue;
+    }
     dst[4 * g] = a.x * inv;
     dst[4 * g + 1] = a.y * inv;
     dst[4 * g + 2] = a.z * inv;

@@ -116,6 +116,9 @@ cudaError_t launch_map_candidates(int32_t* out_idx, const int32_t* cand_idx, int
                                   const int64_t* ent_off, const int32_t* q_seq, const uint8_t* pf_rows,
                                   int64_t pf_row_bytes, cudaStream_t stream);
 
+// Flag bits of hybrid_decode_attn's mode.
+constexpr int kAttnFlags = CSKV_ATTN_PAIRS | CSKV_ATTN_KV_FP8 | CSKV_ATTN_KV_FP4 | CSKV_ATTN_OUT_BF16;
+
 // attention.cu
 struct AttnParams {
   int mode;
@@ -138,10 +141,12 @@ struct AttnParams {
   int cluster;  // tensor-core kernel: the splits of a query form a cluster of this size (0: merge kernel)
   int pairs;    // tensor-core HCA kernel: CTA row y takes queries 2y, 2y + 1 (adjacent positions)
   int Hv;       // heads of a unit of work: H, or 2H for a pair (its rows 0..H-1, then H..2H-1)
-  int kv8;      // CUDA-core kernel: kv_cmp rows are FP8 main-KV rows (kv8.cuh), kv_raw rows plain
+  int kv8;      // kv_cmp rows are FP8 main-KV rows (kv8.cuh), kv_raw rows plain
+  int kv4;      // kv_cmp rows are 4-bit main-KV rows (mx4.cuh), kv_raw rows plain
+  int out_bf16;  // out holds bf16
   float* part_acc;
   float* part_ml;
-  float* out;
+  float* out;   // fp32, or bf16 with out_bf16
   float* lse;
   int* st;
 };
@@ -152,6 +157,9 @@ int attn_tc_cluster_fit(int want);
 cudaError_t launch_attn_combine(const AttnParams& p, cudaStream_t stream);
 int attn_rows_per_split(int mode, int T, int k, int window, int64_t max_entries, int sms);
 int attn_max_splits(int mode, int k, int window, int64_t max_entries, int R);
+// attention_kv4.cu
+void attn_kv4_plan(int T, int64_t rows_max, int most, int sms, int* R, int* S);
+cudaError_t launch_attn_kv4(const AttnParams& p, int sms, cudaStream_t stream);
 // api.cu: host-side argument checks of hybrid_decode_attn (all but the workspace)
 int check_attn_args(int mode, const void* q, const void* kv_cmp, const int64_t* cmp_off, const int32_t* idx, int k,
                     const void* kv_raw, const int64_t* raw_off, int window, float scale, const int32_t* q_seq,

@@ -59,6 +59,8 @@ enum cskv_mode { CSKV_CSA = 0, CSKV_HCA = 1 };
 /* OR-ed into hybrid_decode_attn's mode (see there): queries 2j and 2j + 1 are adjacent. */
 #define CSKV_ATTN_PAIRS 0x100
 #define CSKV_ATTN_KV_FP8 0x200  /* hybrid_decode_attn: kv_cmp rows are FP8 main-KV rows */
+#define CSKV_ATTN_KV_FP4 0x400  /* hybrid_decode_attn: kv_cmp rows are 4-bit main-KV rows */
+#define CSKV_ATTN_OUT_BF16 0x800  /* hybrid_decode_attn: out is bf16 */
 #define CSKV_KV8_ROW_BYTES 336  /* bytes of one FP8 main-KV row (kv_quantize_fp8) */
 #define CSKV_KV4_ROW_BYTES 176  /* bytes of one 4-bit main-KV row (kv_quantize_fp4) */
 
@@ -393,7 +395,7 @@ CSKV_API size_t lindex_workspace_size_scan(int T, int64_t max_entries);
  *           (1/sqrt(d) typical); anything else is CSKV_ERR_INVALID_ARG.
  * q_seq   : [T] int32; q_pos: [T] int64.
  * max_entries : host; mode HCA: >= every visible HCA entry count; mode CSA: unused.
- * out     : [T, H, d] fp32;  lse: [T, H] fp32 or NULL.
+ * out     : [T, H, d] fp32 (bf16 with CSKV_ATTN_OUT_BF16);  lse: [T, H] fp32 or NULL.
  * workspace : hybrid_attn_workspace_size(...) bytes (no zero-fill needed).
  * mode | CSKV_ATTN_PAIRS : the caller states that queries 2j and 2j + 1 (j < T/2) are the
  *           same sequence's consecutive positions p, p + 1 (a prefill chunk; with an odd T the
@@ -409,6 +411,13 @@ CSKV_API size_t lindex_workspace_size_scan(int T, int64_t max_entries);
  *           row, indexed by cmp_off like the plain rows); kv_raw stays in dtype.  The rows
  *           are decoded as they are loaded, on the CUDA cores (the tensor-core kernel takes
  *           plain rows only; ignores CSKV_ATTN_PAIRS).  The workspace size is the same.
+ * mode | CSKV_ATTN_KV_FP4 : kv_cmp holds 4-bit main-KV rows (kv_quantize_fp4: 176 bytes a row,
+ *           indexed by cmp_off like the plain rows); kv_raw stays in dtype.  bf16 queries run on
+ *           the tensor cores over the rows decoded to bf16 (exact), fp32 ones on the CUDA cores;
+ *           CSKV_ATTN_PAIRS is ignored.  The workspace size is the same.  Not together with
+ *           CSKV_ATTN_KV_FP8.  out must be 16-byte aligned.
+ * mode | CSKV_ATTN_OUT_BF16 : out is [T, H, d] bf16 (16-byte aligned), rounded to nearest even
+ *           from the fp32 result; lse stays fp32.
  * ------------------------------------------------------------------------ */
 CSKV_API int hybrid_decode_attn(int mode, const void* q, const void* kv_cmp, const int64_t* cmp_off,
                        const int32_t* idx, int k, const void* kv_raw, const int64_t* raw_off,
