@@ -14,14 +14,15 @@
 // queries it is bound by arithmetic on all three pipes, so one persistent CTA an SM keeps them
 // busy at once with specialised warps; for a few queries it is a latency chain, so a query's rows
 // are split over the SMs.
-//   warp 13     resolves row lists into a table of row addresses, up to four chunks ahead
-//   warps 4-11  load rows (16 bytes of codes a lane, the next chunk's loads in flight while this
-//               one is decoded), decode to bf16 and store them in the 128-byte-swizzle layout
-//   warp 12     one thread issues S = Q K^T and O (+)= P V; Q and P are A operands in tensor
+//   warp 19     resolves row lists into a table of row addresses, up to four chunks ahead
+//   warps 16-17 copy the stored rows to shared memory, up to two chunks ahead
+//   warps 8-15  decode them to bf16 in the 128-byte-swizzle layout, 16 rows a warp
+//   warp 18     one thread issues S = Q K^T and O (+)= P V; Q and P are A operands in tensor
 //               memory, so only K and V are read from shared memory
-//   warps 0-3   softmax: TMEM lane h is head h; S -> P in place, O rescaled when the running
+//   warps 0-7   softmax: TMEM lane h is head h; S -> P in place, O rescaled when the running
 //               maximum grows by more than 2^8 (any reference serves the online softmax), output
-// Two chunk buffers (64 KB each) and two S / P buffers pipeline the chunks, across queries too.
+// Two K and three V buffers (32 KB each) and two S / P buffers pipeline the chunks, across queries
+// too.  The roles' loops are kept short: unrolled ones missed the instruction cache.
 #include "attn_rows.cuh"
 #include "mx4.cuh"
 #include "sm100.cuh"
@@ -29,41 +30,52 @@
 namespace cskv {
 
 constexpr int k4Chunk = 128;                            // rows of a chunk
-constexpr int k4GatherWarps = 8, k4GatherThreads = 32 * k4GatherWarps;
-constexpr int k4Mma = 4 + k4GatherWarps, k4Resolve = k4Mma + 1;
-constexpr int k4Threads = 32 * (k4Resolve + 1);
-constexpr int k4Table = 4;                              // chunks the row table holds
+constexpr int k4SoftWarps = 8, k4GatherWarps = 8;       // four for K, four for V, 32 rows each
+constexpr int k4Copy = k4SoftWarps + k4GatherWarps, k4CopyWarps = 2, k4Mma = k4Copy + 2, k4Resolve = k4Copy + 3;
+constexpr int k4Threads = 32 * 20;
+constexpr int k4Table = 4;                              // chunks the row table (and their notes) hold
+constexpr int k4KStages = 2, k4VStages = 3, k4RawStages = 2;
 constexpr uint32_t k4Region = 128 * 128;                // 128 rows x 128 bytes: one swizzled region
-constexpr uint32_t k4Stage = 4 * k4Region;              // K dims 0-63, 64-127, V dims 0-63, 64-127
-constexpr size_t k4Smem = 2 * (size_t)k4Stage + 1024;
+constexpr uint32_t k4Half = 2 * k4Region;               // a chunk's K (or V): dims 0-63, 64-127
+constexpr uint32_t k4OffV = k4KStages * k4Half, k4OffRaw = k4OffV + k4VStages * k4Half;
+constexpr uint32_t k4Raw = k4Chunk * kKv4RowBytes;      // a chunk's rows as stored
+constexpr size_t k4Smem = k4OffRaw + k4RawStages * k4Raw + 1024;
 constexpr uint32_t k4ColO = 256, k4ColQ = 384;          // TMEM: S/P buffers at 0 and 128, O, Q
+constexpr long long k4WaitCycles = 1LL << 31;           // about a second: a wait gives up
 constexpr float k4Grow = 8.f;                           // log2: growth of the maximum that rescales
 
 struct K4Chunk {
   int nc;            // MMA rows: the chunk's rows rounded up to 16 (0: none)
   int last;          // last chunk of its (query, split)
-  int raw;           // holds raw window rows
   uint32_t mask[4];  // bit r: row r is attended
+  uint32_t raw[4];   // bit r: row r is a bf16 window row
 };
 
 struct K4Shared {
-  uint64_t tab_full[k4Table], tab_empty[k4Table], kv_full[2], kv_empty[2], s_full[2], p_full[2], o_done, q_full, bail;
+  uint64_t tab_full[k4Table], tab_empty[k4Table], k_full[k4KStages], k_empty[k4KStages], v_full[k4VStages];
+  uint64_t raw_full[k4RawStages], raw_empty[k4RawStages];
+  uint64_t v_empty[k4VStages], s_full[2], p_full[2], max_full[4], sum_full[4], o_done, q_full, bail;
   uint32_t tmem;
   int abort;
-  K4Chunk tab_meta[k4Table], meta[2];
-  uint64_t row[k4Table][k4Chunk];  // row address; 0 skipped; bit 0: a raw bf16 row
+  K4Chunk tab_meta[k4Table], meta[k4Table];
+  float half_max[2][2][128], half_sum[2][128];  // [chunk parity][column half][head], [half][head]
+  uint64_t row[k4Table][k4Chunk];               // address of each row; 0: skipped
 };
 
 // Waits for phase `phase` of a barrier.  Bounded: one role that gives up makes every role of the
-// CTA leave its loop.
-__device__ __forceinline__ bool k4_wait(K4Shared& sh, uint64_t* bar, uint32_t phase, int* st) {
-  for (int i = 0; i < (1 << 22); ++i) {
-    if (mbar_try_wait(bar, phase & 1u)) return true;
-    if (*(volatile int*)&sh.abort) return false;
-  }
-  *(volatile int*)&sh.abort = 1;
+// CTA leave its loop.  The waiting loop is one function for all sites, to keep their code short.
+__device__ __noinline__ bool k4_wait_slow(uint64_t* bar, uint32_t parity, int* abort, int* st) {
+  const long long t0 = clock64();
+  do {
+    if (mbar_poll(bar, parity)) return true;
+    if (*(volatile int*)abort) return false;
+  } while (clock64() - t0 < k4WaitCycles);
+  *(volatile int*)abort = 1;
   flag(st, CSKV_DEV_TIMEOUT);
   return false;
+}
+__device__ __forceinline__ bool k4_wait(K4Shared& sh, uint64_t* bar, uint32_t phase, int* st) {
+  return mbar_try_wait(bar, phase & 1u) || k4_wait_slow(bar, phase & 1u, &sh.abort, st);
 }
 // The same for a whole warp, whose lanes agree on the answer.
 __device__ __forceinline__ bool k4_wait_warp(K4Shared& sh, uint64_t* bar, uint32_t phase, int* st) {
@@ -113,16 +125,44 @@ __device__ __forceinline__ uint4 e4m3x8_bf16(uint32_t w0, uint32_t w1, uint32_t 
                     e4m3x2_bf16(prmt(w1, 0u, 0x1404u), s), e4m3x2_bf16(prmt(w1, 0u, 0x3424u), s));
 }
 
-// Byte offset of 16-byte piece c (0..31 of the 512-byte bf16 row) of row r in a chunk buffer.
+// Byte offset of 16-byte piece c (0..15 of 128 bf16 dims) of row r in a K or V buffer.
 __device__ __forceinline__ uint32_t k4_off(int r, int c) {
   return (uint32_t)(c >> 3) * k4Region + (uint32_t)r * 128 + ((uint32_t)((c & 7) ^ (r & 7)) << 4);
 }
-
-// One thread's share of a chunk's codes: three E2M1 blocks and one E4M3 block.
-struct K4Codes {
-  uint4 c4[3], c8[2];
-  uint32_t e[4];  // scale codes; bit 8: the row is skipped, bit 9: not a 4-bit row of this chunk
-};
+// Shared memory by 32-bit addresses (generic ones cost twice the arithmetic).
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// 16 bytes, or zeros with bytes = 0.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// One E2M1 block: 16 bytes of codes at `src`, its scale code at `scale` -> four 16-byte pieces at
+// `to`, whose places differ by xor.
+__device__ __forceinline__ void put_e2m1_block(uint32_t src, uint32_t scale, uint32_t to) {
+  const uint4 c = lds128(src);
+  const uint32_t s = scale_bf16x2(lds_u8(scale));
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int v = 0; v < 4; ++v) sts128(to ^ (16u * v), e2m1x8_bf16(w[v], s));
+}
+// Sixteen E4M3 codes -> two pieces.
+__device__ __forceinline__ void put_e4m3_half(uint32_t src, uint32_t scale, uint32_t to) {
+  const uint4 c = lds128(src);
+  const uint32_t s = scale_bf16x2(lds_u8(scale));
+  sts128(to, e4m3x8_bf16(c.x, c.y, s));
+  sts128(to ^ 16u, e4m3x8_bf16(c.z, c.w, s));
+}
 
 __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_constant__ AttnParams p) {
   extern __shared__ __align__(1024) uint8_t smraw[];
@@ -132,6 +172,8 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
   const int S = p.max_splits, H = p.H;
   const int64_t items = (int64_t)p.T * S;
 
+  const int quads = (H + 31) / 32, soft = 2 * quads;  // TMEM lane groups with heads, softmax warps at work
+
   // ---- set-up that reads no input overlaps the previous kernel (dependent launch)
   if (warp == k4Mma) {
     tmem_alloc(&sh.tmem, 512);
@@ -140,16 +182,30 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
   if (tid == 0) {
     for (int i = 0; i < k4Table; ++i) {
       mbar_init(&sh.tab_full[i], 1);
-      mbar_init(&sh.tab_empty[i], k4GatherWarps);
+      mbar_init(&sh.tab_empty[i], k4GatherWarps + k4CopyWarps);
+    }
+    for (int i = 0; i < k4RawStages; ++i) {
+      mbar_init(&sh.raw_full[i], 32 * k4CopyWarps);
+      mbar_init(&sh.raw_empty[i], k4GatherWarps);
+    }
+    for (int i = 0; i < k4KStages; ++i) {
+      mbar_init(&sh.k_full[i], k4GatherWarps / 2);
+      mbar_init(&sh.k_empty[i], 1);
+    }
+    for (int i = 0; i < k4VStages; ++i) {
+      mbar_init(&sh.v_full[i], k4GatherWarps / 2);
+      mbar_init(&sh.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.kv_full[i], k4GatherWarps);
-      mbar_init(&sh.kv_empty[i], 1);
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.s_full[i], 2);
+      mbar_init(&sh.p_full[i], soft);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh.max_full[i], 2);
+      mbar_init(&sh.sum_full[i], 2);
     }
     mbar_init(&sh.o_done, 1);
-    mbar_init(&sh.q_full, 4);
+    mbar_init(&sh.q_full, soft);
     mbar_init(&sh.bail, 1);
     sh.abort = 0;
     fence_mbar_init();
@@ -160,293 +216,316 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
   const uint32_t tmem = sh.tmem;
   pdl_wait();
 
-  if (warp == k4Resolve) {
-    // ---------------------------------------------------------------- row lists
-    uint32_t g = 0;
-    bool ok = true;
-    for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const int t = (int)(item / S), split = (int)(item % S);
-      const QueryRows q = query_rows(p, t);
-      if (q.s < 0 && split == 0 && lane == 0) flag(p.st, CSKV_DEV_BAD_INDEX);
-      const int64_t r0 = (int64_t)split * p.rows_per_split;
-      const int64_t r1 = q.s < 0 ? r0 : max(r0, min(q.n_rows, r0 + p.rows_per_split));
-      if (q.s >= 0 && split == S - 1 && lane == 0 && q.n_rows > r0 + p.rows_per_split) flag(p.st, CSKV_DEV_CAPACITY);
-      const int chunks = max(1, (int)((r1 - r0 + k4Chunk - 1) / k4Chunk));
-      // the selected entries of a chunk load one chunk ahead
-      int64_t e[4];
-      const bool csa = p.mode == CSKV_CSA;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t r = r0 + 32 * j + lane;
-        e[j] = csa && r < r1 && r < q.n_cmp ? (int64_t)__ldg(p.idx + (size_t)t * p.k + r) : -2;
-      }
-      for (int c = 0; c < chunks && ok; ++c, ++g) {
-        const int64_t a = r0 + (int64_t)c * k4Chunk;
-        const int rows = (int)min((int64_t)k4Chunk, r1 - a);
-        const int slot = g % k4Table;
-        if (g >= k4Table) ok = k4_wait_warp(sh, &sh.tab_empty[slot], g / k4Table - 1, p.st);
-        if (!ok) break;
-        uint32_t raw_any = 0;
+  if (warp >= k4SoftWarps + k4GatherWarps) {
+    if (warp == k4Resolve) {
+      // ---------------------------------------------------------------- row lists
+      uint32_t g = 0;
+      bool ok = true;
+      for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
+        const int t = (int)(item / S), split = (int)(item % S);
+        const QueryRows q = query_rows(p, t);
+        if (q.s < 0 && split == 0 && lane == 0) flag(p.st, CSKV_DEV_BAD_INDEX);
+        const int64_t r0 = (int64_t)split * p.rows_per_split;
+        const int64_t r1 = q.s < 0 ? r0 : max(r0, min(q.n_rows, r0 + p.rows_per_split));
+        if (q.s >= 0 && split == S - 1 && lane == 0 && q.n_rows > r0 + p.rows_per_split) flag(p.st, CSKV_DEV_CAPACITY);
+        const int chunks = max(1, (int)((r1 - r0 + k4Chunk - 1) / k4Chunk));
+        // the selected entries of a chunk load one chunk ahead
+        int32_t e[4];
+        const bool csa = p.mode == CSKV_CSA;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int r = 32 * j + lane;
-          int64_t off = -1;
-          bool is_raw = false;
-          if (r < rows) off = resolve_row(p, q, t, a + r, &is_raw, e[j] < -1 ? (int64_t)-2 : e[j]);
-          uint64_t at = 0;
-          if (off >= 0)
-            at = is_raw ? reinterpret_cast<uint64_t>(reinterpret_cast<const __nv_bfloat16*>(p.kv_raw) + off) | 1u
-                        : reinterpret_cast<uint64_t>(p.kv_cmp) + (uint64_t)(off / kRow) * kKv4RowBytes;
-          sh.row[slot][r] = at;
-          const uint32_t m = __ballot_sync(0xffffffffu, off >= 0);
-          raw_any |= __ballot_sync(0xffffffffu, off >= 0 && is_raw);
-          if (lane == 0) sh.tab_meta[slot].mask[j] = m;
-          const int64_t rn = a + k4Chunk + r;
-          e[j] = csa && rn < r1 && rn < q.n_cmp ? (int64_t)__ldg(p.idx + (size_t)t * p.k + rn) : -2;
+          const int64_t r = r0 + 32 * j + lane;
+          e[j] = csa && r < r1 && r < q.n_cmp ? __ldg(p.idx + (size_t)t * p.k + r) : -2;
         }
-        if (lane == 0) {
-          sh.tab_meta[slot].nc = max(0, (rows + 15) & ~15);
-          sh.tab_meta[slot].last = c == chunks - 1;
-          sh.tab_meta[slot].raw = raw_any != 0;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.tab_full[slot]);
-      }
-    }
-  } else if (warp >= 4 && warp < k4Mma) {
-    // ---------------------------------------------------------------- rows -> bf16 in shared memory
-    const int gt = tid - 128, gw = warp - 4;
-    // E2M1 blocks i = gt + 256 j of the chunk's 768: row i / 6, block i % 6 (K blocks 0, 1, V
-    // blocks 4..7); the E4M3 block: row gt / 2, block 2 + gt % 2
-    const int r8 = gt >> 1, b8 = 2 + (gt & 1);
-    auto load = [&](uint32_t g, K4Codes& k) {
-      const int slot = g % k4Table;
-      const int nc = sh.tab_meta[slot].nc;
+        for (int c = 0; c < chunks && ok; ++c, ++g) {
+          const int64_t a = r0 + (int64_t)c * k4Chunk;
+          const int rows = (int)min((int64_t)k4Chunk, r1 - a);
+          const int slot = g % k4Table;
+          if (g >= k4Table) ok = k4_wait_warp(sh, &sh.tab_empty[slot], g / k4Table - 1, p.st);
+          if (!ok) break;
+          int32_t en[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = gt + k4GatherThreads * j;
-        const int r = j < 3 ? i / 6 : r8;
-        const int b6 = i % 6, b = j < 3 ? (b6 < 2 ? b6 : b6 + 2) : b8;
-        const uint64_t at = r < nc ? sh.row[slot][r] : 1;
-        const uint8_t* row = reinterpret_cast<const uint8_t*>(at);
-        k.e[j] = at == 0 ? 0x100u : (at & 1) ? 0x200u : 0u;
-        if (k.e[j] == 0) {
-          k.e[j] = __ldg(row + kKv4Scales + b);
-          if (j < 3) {
-            k.c4[j] = __ldg(reinterpret_cast<const uint4*>(row + (b < 2 ? 16 * b : kKv4V + 16 * (b - 4))));
-          } else {
-            k.c8[0] = __ldg(reinterpret_cast<const uint4*>(row + kKv4Rope + 32 * (b - 2)));
-            k.c8[1] = __ldg(reinterpret_cast<const uint4*>(row + kKv4Rope + 32 * (b - 2)) + 1);
+          for (int j = 0; j < 4; ++j) {
+            const int64_t rn = a + k4Chunk + 32 * j + lane;
+            en[j] = csa && rn < r1 && rn < q.n_cmp ? __ldg(p.idx + (size_t)t * p.k + rn) : -2;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = 32 * j + lane;
+            int64_t off = -1;
+            bool is_raw = false;
+            if (r < rows) off = resolve_row(p, q, t, a + r, &is_raw, e[j] < -1 ? (int64_t)-2 : (int64_t)e[j]);
+            uint64_t at = 0;
+            if (off >= 0)
+              at = is_raw ? reinterpret_cast<uint64_t>(reinterpret_cast<const __nv_bfloat16*>(p.kv_raw) + off)
+                          : reinterpret_cast<uint64_t>(p.kv_cmp) + (uint64_t)off / kRow * kKv4RowBytes;
+            sh.row[slot][r] = at;
+            const uint32_t m = __ballot_sync(0xffffffffu, off >= 0), mr = __ballot_sync(0xffffffffu, off >= 0 && is_raw);
+            if (lane == 0) sh.tab_meta[slot].mask[j] = m, sh.tab_meta[slot].raw[j] = mr;
+            e[j] = en[j];
+          }
+          if (lane == 0) {
+            sh.tab_meta[slot].nc = max(0, (rows + 15) & ~15);
+            sh.tab_meta[slot].last = c == chunks - 1;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.tab_full[slot]);
+        }
+      }
+    } else if (warp < k4Mma) {
+      // -------------------------------------------------------------- stored rows -> shared memory
+      // As they are, 11 pieces of 16 bytes a row, neighbouring lanes on neighbouring pieces (a bulk
+      // copy a row took 75 cycles each).  Skipped and window rows: zeros, which decode as zeros.
+      const int first = (warp - k4Copy) * (k4Chunk / k4CopyWarps);
+      uint32_t g = 0;
+      bool ok = true;
+      for (int64_t item = blockIdx.x; item < items && ok; ++g) {
+        const uint32_t slot = g % k4Table, sr = g % k4RawStages;
+        ok = k4_wait_warp(sh, &sh.tab_full[slot], g / k4Table, p.st) &&
+             (g < k4RawStages || k4_wait_warp(sh, &sh.raw_empty[sr], g / k4RawStages - 1, p.st));
+        if (!ok) break;
+        const K4Chunk& m = sh.tab_meta[slot];
+        if (m.last) item += gridDim.x;
+        const uint32_t dst = smem_u32(buf) + k4OffRaw + sr * k4Raw + first * kKv4RowBytes;
+#pragma unroll 1
+        for (int w = 0; w < 2; ++w) {
+          if (first + 32 * w >= m.nc) continue;
+          const uint32_t have = m.mask[(first >> 5) + w] & ~m.raw[(first >> 5) + w];
+          // 32 rows: 352 pieces, 11 a lane; the addresses first, so that the copies follow one another
+          const uint8_t* at[11];
+#pragma unroll
+          for (int i = 0; i < 11; ++i) {
+            const int x = lane + 32 * i, r = x / 11;
+            at[i] = (have >> r) & 1u
+                        ? reinterpret_cast<const uint8_t*>(sh.row[slot][first + 32 * w + r]) + 16 * (x - 11 * r)
+                        : nullptr;
+          }
+#pragma unroll
+          for (int i = 0; i < 11; ++i)
+            cp16(dst + (w * 32 * 11 + lane + 32 * i) * 16, at[i] ? (const void*)at[i] : p.kv_cmp, at[i] ? 16u : 0u);
+        }
+        cp_async_arrive(&sh.raw_full[sr]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.tab_empty[slot]);
+      }
+      cp_async_wait_all();
+    } else if (warp == k4Mma) {
+      // ---------------------------------------------------------------- MMA issue
+      if (lane == 0) {
+        const uint32_t kv = smem_u32(buf);
+        uint32_t g = 0, n = 0;
+        bool ok = true;
+        auto issue_s = [&](uint32_t c) {
+          const uint32_t st = c % k4KStages;
+          if (!k4_wait(sh, &sh.k_full[st], c / k4KStages, p.st)) return false;
+          tc_fence_after();
+          const int nc = sh.meta[c % k4Table].nc;
+          if (nc) {
+            const uint32_t idesc = idesc_bf16_f32(128, nc, false, false);
+#pragma unroll 1
+            for (int kk = 0; kk < 8; ++kk)
+              tc_mma_f16_ta(tmem + (c & 1) * 128, tmem + k4ColQ + kk * 8,
+                            smem_desc_sw128(kv + st * k4Half + (uint32_t)(kk >> 2) * k4Region + (uint32_t)(kk & 3) * 32,
+                                            16, 1024),
+                            idesc, kk > 0);
+          }
+          tc_commit(&sh.k_empty[st]);
+          tc_commit(&sh.s_full[c & 1]);
+          mbar_arrive(&sh.s_full[c & 1]);  // passes the chunk's notes on to the softmax warps
+          return true;
+        };
+        for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x, ++n) {
+          ok = k4_wait(sh, &sh.q_full, n, p.st);
+          tc_fence_after();
+          ok = ok && issue_s(g);
+          bool first = true;
+          for (bool more = true; more && ok; ++g) {
+            const uint32_t st = g % k4VStages;
+            const int nc = sh.meta[g % k4Table].nc;
+            more = !sh.meta[g % k4Table].last;
+            // the next chunk's S goes first if its K is there before this chunk's P
+            bool ahead = false;
+            if (more) {
+              for (int i = 0; i < (1 << 22) && !ahead && !mbar_test(&sh.p_full[g & 1], (g >> 1) & 1u); ++i) {
+                if (mbar_try_wait(&sh.k_full[(g + 1) % k4KStages], ((g + 1) / k4KStages) & 1u)) {
+                  ahead = true;
+                  ok = issue_s(g + 1);
+                }
+              }
+            }
+            ok = ok && k4_wait(sh, &sh.v_full[st], g / k4VStages, p.st) && k4_wait(sh, &sh.p_full[g & 1], g >> 1, p.st);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t idesc = idesc_bf16_f32(128, 128, false, true);
+#pragma unroll 1
+            for (int kk = 0; kk < nc / 16; ++kk)
+              tc_mma_f16_ta(tmem + k4ColO, tmem + (g & 1) * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+                            smem_desc_sw128(kv + k4OffV + st * k4Half + (uint32_t)kk * 2048, k4Region, 1024), idesc,
+                            !first || kk > 0);
+            if (nc) first = false;
+            tc_commit(&sh.v_empty[st]);
+            tc_commit(&sh.o_done);
+            if (more && !ahead) ok = issue_s(g + 1);
           }
         }
+        if (!ok) {  // gave up: nothing of this CTA may still be in flight when its memory is released
+          tc_commit(&sh.bail);
+          mbar_wait_bounded(&sh.bail, 0);
+        }
       }
-    };
+      __syncwarp();
+    }
+  } else if (warp >= k4SoftWarps) {
+    // ---------------------------------------------------------------- rows -> bf16 in shared memory
+    // Warps 0-3 of the eight decode K, the others V, 32 rows each, a few rows at a time through
+    // short loops.  E2M1: sixteen rows' K blocks (lane l: row l % 16, block l / 16) or eight rows'
+    // V blocks (row l % 8, block l / 8); E4M3: eight rows' sixteen codes (row l % 8, piece l / 8).
+    // Eight neighbouring lanes hold the same piece of eight rows: their swizzled stores meet all
+    // banks once, and so do their loads of rows 176 bytes apart.
+    const int gw = (warp - k4SoftWarps) & 3, l8 = lane & 7, l16 = lane & 15, pv = lane >> 3, pk = lane >> 4;
+    const bool is_v = warp >= k4SoftWarps + 4;
+    const int row0 = gw * 32;
+    const uint32_t base = smem_u32(buf), raw_base = base + k4OffRaw + row0 * kKv4RowBytes;
     uint32_t g = 0;
     bool ok = true;
-    int64_t item = blockIdx.x;
-    K4Codes cur, nxt;
-    if (item < items) {
-      ok = k4_wait_warp(sh, &sh.tab_full[0], 0, p.st);
-      if (ok) load(0, cur);
-    }
-    while (item < items && ok) {
-      const int slot = g % k4Table, st = g & 1;
-      const K4Chunk meta = sh.tab_meta[slot];
-      if (meta.last) item += gridDim.x;
-      if (item < items) {  // there is a next chunk: its loads go out before this one is decoded
-        ok = k4_wait_warp(sh, &sh.tab_full[(g + 1) % k4Table], (g + 1) / k4Table, p.st);
-        if (!ok) break;
-        load(g + 1, nxt);
-      }
-      if (g >= 2) ok = k4_wait_warp(sh, &sh.kv_empty[st], (g >> 1) - 1, p.st);
+    for (int64_t item = blockIdx.x; item < items && ok; ++g) {
+      const uint32_t slot = g % k4Table, sr = g % k4RawStages, sk = g % k4KStages, sv = g % k4VStages;
+      ok = k4_wait_warp(sh, &sh.tab_full[slot], g / k4Table, p.st) &&
+           k4_wait_warp(sh, &sh.raw_full[sr], g / k4RawStages, p.st) &&
+           (is_v ? (g < k4VStages || k4_wait_warp(sh, &sh.v_empty[sv], g / k4VStages - 1, p.st))
+                 : (g < k4KStages || k4_wait_warp(sh, &sh.k_empty[sk], g / k4KStages - 1, p.st)));
       if (!ok) break;
-      uint8_t* dst = buf + st * k4Stage;
-      if (meta.raw) {
-        // window rows: a warp copies whole 512-byte rows, a lane 16 bytes
-        for (int r = gw; r < meta.nc; r += k4GatherWarps) {
-          const uint64_t at = sh.row[slot][r];
-          if (at & 1) cp_async16(dst + k4_off(r, lane), reinterpret_cast<const uint8_t*>(at - 1) + 16 * lane, 16u);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (cur.e[j] & 0x200u) continue;
-        const int i = gt + k4GatherThreads * j;
-        const int r = j < 3 ? i / 6 : r8;
-        const int b6 = i % 6, b = j < 3 ? (b6 < 2 ? b6 : b6 + 2) : b8;
-        const bool skip = cur.e[j] & 0x100u;
-        const uint32_t s = scale_bf16x2(cur.e[j] & 0xFFu);
-        // the four pieces of a block in an order that differs between the lanes of a row, so that
-        // a quarter warp's stores meet different banks
-        const int rot = j < 3 ? b6 >> 1 : 0;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          uint4 o = make_uint4(0u, 0u, 0u, 0u);
-          int pc;
-          if (j < 3) {
-            pc = (v + rot) & 3;
-            const uint4 c = cur.c4[j];
-            const uint32_t w = pc == 0 ? c.x : pc == 1 ? c.y : pc == 2 ? c.z : c.w;
-            if (!skip) o = e2m1x8_bf16(w, s);
+      const K4Chunk& m = sh.tab_meta[slot];
+      if (m.last) item += gridDim.x;
+      const uint32_t raw = m.raw[gw];  // window rows among this warp's 32
+      const uint32_t src = raw_base + sr * k4Raw;
+      const uint32_t dst = base + (is_v ? k4OffV + sv * k4Half : sk * k4Half);
+      if (row0 < m.nc) {
+        if (raw != 0xFFFFFFFFu) {
+          if (is_v) {
+            uint32_t at = src + l8 * kKv4RowBytes, to = dst + k4_off(row0 + l8, 4 * pv);
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j, at += 8 * kKv4RowBytes, to += 8 * 128)
+              put_e2m1_block(at + kKv4V + 16 * pv, at + kKv4Scales + 4 + pv, to);
           } else {
-            pc = v;
-            const uint4 c = cur.c8[v >> 1];
-            if (!skip) o = (v & 1) ? e4m3x8_bf16(c.z, c.w, s) : e4m3x8_bf16(c.x, c.y, s);
+            uint32_t at = src + l16 * kKv4RowBytes, to = dst + k4_off(row0 + l16, 4 * pk);
+#pragma unroll 1
+            for (int j = 0; j < 2; ++j, at += 16 * kKv4RowBytes, to += 16 * 128)
+              put_e2m1_block(at + 16 * pk, at + kKv4Scales + pk, to);
+            at = src + l8 * kKv4RowBytes, to = dst + k4_off(row0 + l8, 8 + 2 * pv);
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j, at += 8 * kKv4RowBytes, to += 8 * 128)
+              put_e4m3_half(at + kKv4Rope + 16 * pv, at + kKv4Scales + 2 + (pv >> 1), to);
           }
-          *reinterpret_cast<uint4*>(dst + k4_off(r, 4 * b + pc)) = o;
+        }
+        if (raw) {
+          // window rows: a half warp copies half a row (16 bytes a lane) straight to its place, over
+          // the zeros decoded for it
+          __syncwarp();
+#pragma unroll 1
+          for (int r = pk; r < 32; r += 2)
+            if ((raw >> r) & 1u)
+              cp16(dst + k4_off(row0 + r, l16),
+                   reinterpret_cast<const uint8_t*>(sh.row[slot][row0 + r]) + (is_v ? 256 : 0) + 16 * l16, 16u);
+          cp_async_wait_all();
         }
       }
-      if (gt == 0) sh.meta[st] = meta;
-      if (meta.raw) cp_async_wait_all();
+      if (warp == k4SoftWarps && lane == 0) sh.meta[slot] = m;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
+        mbar_arrive(is_v ? &sh.v_full[sv] : &sh.k_full[sk]);
+        mbar_arrive(&sh.raw_empty[sr]);
         mbar_arrive(&sh.tab_empty[slot]);
-        mbar_arrive(&sh.kv_full[st]);
-      }
-      cur = nxt;
-      ++g;
-    }
-  } else if (warp == k4Mma) {
-    // ---------------------------------------------------------------- MMA issue
-    if (lane == 0) {
-      const uint32_t kv = smem_u32(buf);
-      uint32_t g = 0, n = 0;
-      bool ok = true;
-      auto issue_s = [&](uint32_t c) {
-        const int st = c & 1;
-        if (!k4_wait(sh, &sh.kv_full[st], c >> 1, p.st)) return false;
-        tc_fence_after();
-        const int nc = sh.meta[st].nc;
-        if (nc) {
-          const uint32_t idesc = idesc_bf16_f32(128, nc, false, false);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc_mma_f16_ta(tmem + st * 128, tmem + k4ColQ + kk * 8,
-                          smem_desc_sw128(kv + st * k4Stage + (uint32_t)(kk >> 2) * k4Region + (uint32_t)(kk & 3) * 32,
-                                          16, 1024),
-                          idesc, kk > 0);
-        }
-        tc_commit(&sh.s_full[st]);
-        return true;
-      };
-      for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x, ++n) {
-        ok = k4_wait(sh, &sh.q_full, n, p.st);
-        tc_fence_after();
-        ok = ok && issue_s(g);
-        bool first = true;
-        for (bool more = true; more && ok; ++g) {
-          const int st = g & 1;
-          const int nc = sh.meta[st].nc;
-          more = !sh.meta[st].last;
-          if (more) ok = issue_s(g + 1);
-          ok = ok && k4_wait(sh, &sh.p_full[st], g >> 1, p.st);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t idesc = idesc_bf16_f32(128, 128, false, true);
-          for (int kk = 0; kk < nc / 16; ++kk)
-            tc_mma_f16_ta(tmem + k4ColO, tmem + st * 128 + kk * 8,
-                          smem_desc_sw128(kv + st * k4Stage + 2 * k4Region + (uint32_t)kk * 2048, k4Region, 1024),
-                          idesc, !first || kk > 0);
-          if (nc) first = false;
-          tc_commit(&sh.kv_empty[st]);
-          tc_commit(&sh.o_done);
-        }
-      }
-      if (!ok) {  // gave up: nothing of this CTA may still be in flight when its memory is released
-        tc_commit(&sh.bail);
-        mbar_wait_bounded(&sh.bail, 0);
       }
     }
-    __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax and output
-    const int h = tid;
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    const bool active = warp * 32 < H;  // a warp without heads only keeps the barriers in step
+    // warps w and w + 4 share the TMEM lanes of heads 32w .. 32w + 31: each takes half of a
+    // chunk's columns, of Q's and of O's dims, and they exchange row maxima and sums
+    const int quad = warp & 3, half = warp >> 2, h = quad * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     const float sl2 = p.scale_log2;
     const float sk = (p.sink && h < H) ? __ldg(p.sink + h) * kLog2e : -INFINITY;
     auto put_q = [&](int64_t item) {
-      if (active) {
+      {
         const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
-                                                          ((size_t)(item / S) * H + h) * kHeadDim);
+                                                          ((size_t)(item / S) * H + h) * kHeadDim + 64 * half);
+        uint32_t v[32];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t v[32];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 w = h < H ? __ldg(src + 8 * half + i) : make_uint4(0u, 0u, 0u, 0u);
-            v[4 * i] = w.x, v[4 * i + 1] = w.y, v[4 * i + 2] = w.z, v[4 * i + 3] = w.w;
-          }
-          tmem_st32(tmem + k4ColQ + lane_base + 32 * half, v);
+        for (int i = 0; i < 8; ++i) {
+          const uint4 w = h < H ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+          v[4 * i] = w.x, v[4 * i + 1] = w.y, v[4 * i + 2] = w.z, v[4 * i + 3] = w.w;
         }
+        tmem_st32(tmem + k4ColQ + lane_base + 32 * half, v);
         tmem_st_wait();
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full);
     };
-    uint32_t g = 0;
+    uint32_t g = 0, n = 0;
     bool ok = true;
-    if (blockIdx.x < items) put_q(blockIdx.x);
-    for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
+    if (quad < quads && blockIdx.x < items) put_q(blockIdx.x);
+    for (int64_t item = quad < quads ? blockIdx.x : items; item < items && ok; item += gridDim.x, ++n) {
       float m = -INFINITY, l = 0.f;
       bool filled = false;  // O holds something
       for (bool more = true; more; ++g) {
-        const int st = g & 1;
-        ok = k4_wait_warp(sh, &sh.kv_full[st], g >> 1, p.st) &&  // the chunk's description
-             k4_wait_warp(sh, &sh.s_full[st], g >> 1, p.st);
+        const uint32_t st = g % k4Table, sp = g & 1;
+        ok = k4_wait_warp(sh, &sh.s_full[sp], g >> 1, p.st);
         if (!ok) break;
         tc_fence_after();
         const int nc = sh.meta[st].nc;
         more = !sh.meta[st].last;
-        const uint32_t tS = tmem + st * 128 + lane_base;
-        if (active && nc) {
-          // pass 1: the row maximum over attended columns (columns past nc hold old values; their
-          // mask bits are clear)
-          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          for (int cc = 0; cc < nc; cc += 32) {
-            const uint32_t vm = sh.meta[st].mask[cc >> 5];
-            uint32_t v[32];
-            tmem_ld32(tS + cc, v);
+        const uint32_t tS = tmem + sp * 128 + 64 * half + lane_base;
+        if (nc) {
+          // this half's 64 columns, 16 at a time; those past nc hold old values, and their mask bits
+          // are clear
+          const uint64_t vm = (uint64_t)sh.meta[st].mask[2 * half + 1] << 32 | sh.meta[st].mask[2 * half];
+          auto columns = [&](int c, uint32_t (&v)[16]) {
+            tmem_ld16(tS + c, v);
             tmem_ld_wait();
-            if (vm == 0xFFFFFFFFu) {
+            const uint32_t b = (uint32_t)(vm >> c) & 0xFFFFu;
+            if (b != 0xFFFFu) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(v[i]));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                mx4[i & 3] = fmaxf(mx4[i & 3], ((vm >> i) & 1u) ? __uint_as_float(v[i]) : -INFINITY);
+              for (int i = 0; i < 16; ++i)
+                if (!((b >> i) & 1u)) v[i] = 0xFF800000u;  // -inf
             }
+          };
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 16) {
+            uint32_t v[16];
+            columns(c, v);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2)
+              mx4[(i >> 1) & 3] = fmaxf(mx4[(i >> 1) & 3], fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
           }
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
+          float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          sh.half_max[sp][half][h] = mx;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.max_full[quad]);
+          ok = k4_wait_warp(sh, &sh.max_full[quad], g, p.st);
+          if (!ok) break;
+          mx = fmaxf(mx, sh.half_max[sp][half ^ 1][h]) * sl2;
           const float m_new = mx > m + k4Grow || m == -INFINITY ? fmaxf(mx, m) : m;
           const float alpha = m_new == -INFINITY || m_new == m ? 1.f : fast_exp2(m - m_new);
           const float nm = m_new == -INFINITY ? 0.f : -m_new;
-          // pass 2: P = 2^(s scale - m) as bf16 over the columns already read
+          // P = 2^(s scale - m) as bf16, over this half's columns that have been read
           float l4[4] = {0.f, 0.f, 0.f, 0.f};
-          for (int cc = 0; cc < nc; cc += 32) {
-            const uint32_t vm = sh.meta[st].mask[cc >> 5];
-            uint32_t v[32], w[16];
-            tmem_ld32(tS + cc, v);
-            tmem_ld_wait();
-            float e[32];
-            if (vm == 0xFFFFFFFFu) {
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 16) {
+            uint32_t v[16], w[8];
+            columns(c, v);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) e[i] = fast_exp2(fmaf(__uint_as_float(v[i]), sl2, nm));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                e[i] = ((vm >> i) & 1u) ? fast_exp2(fmaf(__uint_as_float(v[i]), sl2, nm)) : 0.f;
+            for (int i = 0; i < 8; ++i) {
+              const float e0 = fast_exp2(fmaf(__uint_as_float(v[2 * i]), sl2, nm));
+              const float e1 = fast_exp2(fmaf(__uint_as_float(v[2 * i + 1]), sl2, nm));
+              l4[i & 3] += e0 + e1;
+              const __nv_bfloat162 e = __floats2bfloat162_rn(e0, e1);
+              w[i] = *reinterpret_cast<const uint32_t*>(&e);
             }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) l4[i & 3] += e[i];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(e[2 * i], e[2 * i + 1]);
-              w[i] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-            tmem_st16(tS + (cc >> 1), w);
+            tmem_st8(tS + (c >> 1), w);
           }
           // O of the earlier chunks is rescaled once its last product is complete (tensor-memory
           // accesses are warp-wide, so a warp rescales when one of its rows needs it)
@@ -454,32 +533,41 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
             ok = k4_wait_warp(sh, &sh.o_done, g - 1, p.st);
             if (!ok) break;
             tc_fence_after();
-            for (int cc = 0; cc < 128; cc += 32) {
-              uint32_t v[32];
-              tmem_ld32(tmem + k4ColO + lane_base + cc, v);
+            const uint32_t tO = tmem + k4ColO + lane_base + 64 * half;
+#pragma unroll 1
+            for (int cc = 0; cc < 64; cc += 16) {
+              uint32_t o[16];
+              tmem_ld16(tO + cc, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
-              tmem_st32(tmem + k4ColO + lane_base + cc, v);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st16(tO + cc, o);
             }
           }
           tmem_st_wait();
           l = l * alpha + ((l4[0] + l4[1]) + (l4[2] + l4[3]));
           m = m_new;
+        } else if (lane == 0) {
+          mbar_arrive(&sh.max_full[quad]);
         }
         filled = filled || nc > 0;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[st]);
+        if (lane == 0) mbar_arrive(&sh.p_full[sp]);
       }
       if (!ok) break;
       // every S of this query is complete: the next query's Q may take its place
       if (item + gridDim.x < items) put_q(item + gridDim.x);
-      ok = k4_wait_warp(sh, &sh.o_done, g - 1, p.st);
+      sh.half_sum[half][h] = l;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.sum_full[quad]);
+      ok = k4_wait_warp(sh, &sh.sum_full[quad], n, p.st) && k4_wait_warp(sh, &sh.o_done, g - 1, p.st);
       if (!ok) break;
       tc_fence_after();
+      l += sh.half_sum[half ^ 1][h];
       const int t = (int)(item / S), split = (int)(item % S);
-      if (active && S == 1) {
+      const uint32_t tO = tmem + k4ColO + lane_base + 64 * half;
+      if (S == 1) {
         const float M = fmaxf(m, sk);
         float f = 0.f, L = 0.f;
         if (M != -INFINITY) {
@@ -487,18 +575,19 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
           L = l * f + (p.sink ? exp2f(sk - M) : 0.f);
         }
         const float inv = L > 0.f || L != L ? f / L : 0.f;
-        const size_t row = ((size_t)t * H + h) * kHeadDim;
-        for (int cc = 0; cc < 128; cc += 32) {
-          uint32_t v[32];
+        const size_t row = ((size_t)t * H + h) * kHeadDim + 64 * half;
+#pragma unroll 1
+        for (int cc = 0; cc < 64; cc += 16) {
+          uint32_t v[16];
           __syncwarp();
           if (filled) {
-            tmem_ld32(tmem + k4ColO + lane_base + cc, v);
+            tmem_ld16(tO + cc, v);
             tmem_ld_wait();
           }
           if (h < H) {
             // a row without attended columns has no O of its own
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
+            for (int i = 0; i < 16; i += 8) {
               float o[8];
 #pragma unroll
               for (int j = 0; j < 8; ++j) o[j] = filled && inv != 0.f ? __uint_as_float(v[i + j]) * inv : 0.f;
@@ -509,25 +598,28 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
             }
           }
         }
-        if (h < H && p.lse) p.lse[(size_t)t * H + h] = L > 0.f || L != L ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
-      } else if (active && filled) {
-        // partial for attn_combine_kernel, dimension-major ([split][j][h])
-        const size_t sb = (size_t)t * S + split;
-        float* dst = p.part_acc + sb * kHeadDim * H + h;
-        for (int cc = 0; cc < 128; cc += 32) {
-          uint32_t v[32];
-          __syncwarp();
-          tmem_ld32(tmem + k4ColO + lane_base + cc, v);
-          tmem_ld_wait();
-          if (h < H) {
+        if (half == 0 && h < H && p.lse)
+          p.lse[(size_t)t * H + h] = L > 0.f || L != L ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+      } else {
+        // partial for the merge kernel: [query][split][head][dim], (m, l) [query][split][head] (m =
+        // -inf: no rows, and no partial)
+        const size_t sb = ((size_t)t * S + split) * H + h;
+        float* dst = p.part_acc + sb * kHeadDim + 64 * half;
+        if (filled) {
+#pragma unroll 1
+          for (int cc = 0; cc < 64; cc += 16) {
+            uint32_t v[16];
+            __syncwarp();
+            tmem_ld16(tO + cc, v);
+            tmem_ld_wait();
+            if (h < H) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) dst[(size_t)(cc + i) * H] = __uint_as_float(v[i]);
+              for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<uint4*>(dst + cc + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
           }
         }
-        if (h < H) {
-          p.part_ml[sb * 2 * H + h] = m;
-          p.part_ml[(sb * 2 + 1) * H + h] = l;
-        }
+        if (half == 0 && h < H) reinterpret_cast<float2*>(p.part_ml)[sb] = make_float2(m, l);
       }
       tc_fence_before();
     }
@@ -539,6 +631,61 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// Merges the splits of a query ([TR] §3.1), the sink once ([SW] §十二): M = max(max_s m_s, sink),
+// L = sum_s 2^(m_s - M) l_s + 2^(sink - M), o = sum_s 2^(m_s - M) acc_s / L.  A CTA a head, its four
+// warps a quarter of the splits each, a lane four dims.  Bound by latency: eight splits' loads go
+// out together.
+constexpr int k4MergeWarps = 4;
+
+__global__ void __launch_bounds__(32 * k4MergeWarps) attn_kv4_merge_kernel(const __grid_constant__ AttnParams p) {
+  __shared__ float4 part[k4MergeWarps][32];
+  __shared__ float part_l[k4MergeWarps];
+  const int t = blockIdx.y, h = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int H = p.H, S = p.max_splits;
+  pdl_launch_dependents();
+  pdl_wait();
+  const size_t sb = (size_t)t * S * H + h;
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + sb;
+  const float4* acc = reinterpret_cast<const float4*>(p.part_acc + sb * kHeadDim) + lane;
+  const float sk = p.sink ? __ldg(p.sink + h) * kLog2e : -INFINITY;
+  float M = sk;
+  for (int s = lane; s < S; s += 32) M = fmaxf(M, __ldcg(ml + (size_t)s * H).x);
+  M = warp_max(M);
+  float L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int s = warp; s < S; s += k4MergeWarps) {
+    const float2 x = __ldcg(ml + (size_t)s * H);
+    const float4 a = __ldcg(acc + (size_t)s * H * (kHeadDim / 4));
+    if (x.x != -INFINITY) {
+      const float f = exp2f(x.x - M);
+      L = fmaf(x.y, f, L);
+      o.x = fmaf(a.x, f, o.x), o.y = fmaf(a.y, f, o.y), o.z = fmaf(a.z, f, o.z), o.w = fmaf(a.w, f, o.w);
+    }
+  }
+  part[warp][lane] = o;
+  if (lane == 0) part_l[warp] = L;
+  __syncthreads();
+  if (warp) return;
+#pragma unroll
+  for (int w = 1; w < k4MergeWarps; ++w) {
+    const float4 a = part[w][lane];
+    o.x += a.x, o.y += a.y, o.z += a.z, o.w += a.w;
+    L += part_l[w];
+  }
+  if (p.sink && M != -INFINITY) L += exp2f(sk - M);
+  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+  const size_t dst = ((size_t)t * H + h) * kHeadDim + 4 * lane;
+  if (p.out_bf16) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + dst) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  } else {
+    *reinterpret_cast<float4*>(p.out + dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  }
+  if (lane == 0 && p.lse) p.lse[(size_t)t * H + h] = L > 0.f || L != L ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
 }
 
 // Splits of a query: whole chunks, as many as fill the SMs once; `most` bounds them by the
@@ -562,7 +709,11 @@ cudaError_t launch_attn_kv4(const AttnParams& p, int sms, cudaStream_t stream) {
   e = launch_dependent(attn_kv4_kernel, dim3((unsigned)(items < sms ? items : sms)), dim3(k4Threads), k4Smem, stream, p);
   note_launch();
   if (e != cudaSuccess || p.max_splits == 1) return e;
-  return launch_attn_combine(p, stream);
+  e = ensure_smem(attn_kv4_merge_kernel, 0);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(attn_kv4_merge_kernel, dim3(p.H, p.T), dim3(32 * k4MergeWarps), 0, stream, p);
+  note_launch();
+  return e;
 }
 
 }  // namespace cskv
