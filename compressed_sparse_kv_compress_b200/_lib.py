@@ -17,8 +17,8 @@ F32, BF16, FP8E4M3 = 0, 1, 2
 OVERLAP_PREVIOUS = 1  # csa_compress flags (CSKV_OVERLAP_PREVIOUS)
 ATTN_PAIRS = 0x100  # OR-ed into hybrid_decode_attn's mode (CSKV_ATTN_PAIRS)
 ATTN_KV_FP8 = 0x200  # OR-ed into hybrid_decode_attn's mode (CSKV_ATTN_KV_FP8)
-ATTN_KV_FP4 = 0x400  # OR-ed into hybrid_decode_attn's mode (CSKV_ATTN_KV_FP4)
-ATTN_OUT_BF16 = 0x800  # OR-ed into hybrid_decode_attn's mode (CSKV_ATTN_OUT_BF16)
+ATTN_KV_FP4 = 0x1000  # OR-ed into hybrid_decode_attn's mode (CSKV_ATTN_KV_FP4)
+ATTN_OUT_BF16 = 0x2000  # OR-ed into hybrid_decode_attn's mode (CSKV_ATTN_OUT_BF16)
 KV8_ROW_BYTES = 336  # CSKV_KV8_ROW_BYTES
 KV4_ROW_BYTES = 176  # CSKV_KV4_ROW_BYTES
 CSA, HCA = 0, 1
@@ -45,6 +45,7 @@ SIGNATURES = {
     "kv_quantize_fp8": (_i32, [_p, _i32, _i64, _p, _p]),
     "mxfp4_quantize": (_i32, [_p, _i32, _i64, _i64, _p, _p, _p]),
     "mxfp4_dequantize": (_i32, [_p, _p, _i64, _i64, _i32, _p, _p]),
+    "mxfp4_matmul": (_i32, [_p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _p, _p]),
     "kv_quantize_fp4": (_i32, [_p, _i32, _i64, _p, _i64, _p, _p, _p]),
     "kv_dequantize_fp4": (_i32, [_p, _p, _i64, _i64, _i32, _p, _p, _p]),
     "lindex_pool_keys": (_i32, [_p, _i32, _i32, _p, _p, _i32, _p, _p, _p, _i64, _p, _p, _p, _p]),

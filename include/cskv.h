@@ -59,8 +59,8 @@ enum cskv_mode { CSKV_CSA = 0, CSKV_HCA = 1 };
 /* OR-ed into hybrid_decode_attn's mode (see there): queries 2j and 2j + 1 are adjacent. */
 #define CSKV_ATTN_PAIRS 0x100
 #define CSKV_ATTN_KV_FP8 0x200  /* hybrid_decode_attn: kv_cmp rows are FP8 main-KV rows */
-#define CSKV_ATTN_KV_FP4 0x400  /* hybrid_decode_attn: kv_cmp rows are 4-bit main-KV rows */
-#define CSKV_ATTN_OUT_BF16 0x800  /* hybrid_decode_attn: out is bf16 */
+#define CSKV_ATTN_KV_FP4 0x1000  /* hybrid_decode_attn: kv_cmp rows are 4-bit main-KV rows */
+#define CSKV_ATTN_OUT_BF16 0x2000  /* hybrid_decode_attn: out is bf16 */
 #define CSKV_KV8_ROW_BYTES 336  /* bytes of one FP8 main-KV row (kv_quantize_fp8) */
 #define CSKV_KV4_ROW_BYTES 176  /* bytes of one 4-bit main-KV row (kv_quantize_fp4) */
 
@@ -201,6 +201,26 @@ CSKV_API int mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t D, u
                  cskv_stream_t stream);
 CSKV_API int mxfp4_dequantize(const uint8_t* codes, const uint8_t* bscale, int64_t rows, int64_t D, int dtype,
                  void* out, cskv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * mxfp4_matmul -- product of two MXFP4 matrices on the tensor cores.
+ *
+ * [TR] §4.2 (the indexer projects its queries and keys in low precision), [SW] §六.1: with decoded
+ * values a [M, K] and b [N, K] (rows as mxfp4_quantize writes them, b e.g. a projection's weights,
+ * one row an output),
+ *     out[m, n] = sum_k a[m, k] b[n, k],
+ * exact products, fp32 accumulation, rounded once to out_dtype.
+ * a_codes : [M, K/2] uint8, 16-byte aligned;  a_bscale : [M, K/32] uint8.  b likewise with N.
+ * K       : a multiple of 32, 32 at least.  M, N, K at most 2^30.
+ * out     : [M, N] out_dtype (CSKV_F32 or CSKV_BF16), 16-byte aligned.
+ * Scale rows that are not whole 4-byte words (K % 128, or a base that is not 4-byte aligned) are
+ * read by bytes, which is slower.  M == 0 or N == 0 launches nothing.  Errors:
+ * CSKV_ERR_INVALID_ARG (null or misaligned pointer, bad size or dtype), CSKV_ERR_UNSUPPORTED (FP8
+ * output), CSKV_ERR_LAUNCH.  *dev_status (optional): CSKV_DEV_TIMEOUT.
+ * ------------------------------------------------------------------------ */
+CSKV_API int mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_bscale, const uint8_t* b_codes,
+                 const uint8_t* b_bscale, int64_t M, int64_t N, int64_t K, int out_dtype, void* out,
+                 int* dev_status, cskv_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * kv_quantize_fp4 / kv_dequantize_fp4 -- 4-bit main-KV rows from K||V rows, and back.
