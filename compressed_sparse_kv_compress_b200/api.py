@@ -273,6 +273,21 @@ def mxfp4_dequantize(codes, bscale, out=None, *, dtype=torch.bfloat16, stream=No
     return out
 
 
+def mxfp4_matmul(a_codes, a_bscale, b_codes, b_bscale, out=None, *, dtype=torch.bfloat16, dev_status=None, stream=None):
+    """out [M, N] = a b^T of MXFP4 matrices (mxfp4_quantize): a_codes [M, K/2], a_bscale [M, K/32],
+    b_codes [N, K/2], b_bscale [N, K/32]; out fp32 or bf16 (`dtype`, or out's)."""
+    (M, half), N = a_codes.shape, int(b_codes.shape[0])
+    if out is None:
+        out = torch.empty(M, N, dtype=dtype, device=a_codes.device)
+    _check("mxfp4_matmul", a_codes=(a_codes, torch.uint8, (M, half)), a_bscale=(a_bscale, torch.uint8, (M, half // 16)),
+           b_codes=(b_codes, torch.uint8, (N, half)), b_bscale=(b_bscale, torch.uint8, (N, half // 16)),
+           out=(out, _VALUES, (M, N)), dev_status=(dev_status, torch.int32, (1,)))
+    st = _lib.load().mxfp4_matmul(_ptr(a_codes), _ptr(a_bscale), _ptr(b_codes), _ptr(b_bscale), M, N, 2 * half,
+                                  _dt(out), _ptr(out), _ptr(dev_status), _stream(stream))
+    _lib.check("mxfp4_matmul", st)
+    return out
+
+
 def kv_quantize_fp4(rows, out=None, *, dst=None, dev_status=None, stream=None):
     """4-bit main-KV rows ([cap, 176] uint8) from K||V rows [n, 256] (fp32 or bf16).  dst [n]
     int64: row i goes to out[dst[i]] (negative: left out; no two equal); None: to out[i].  Rows of

@@ -221,6 +221,21 @@ int mxfp4_dequantize(const uint8_t* codes, const uint8_t* bscale, int64_t rows, 
   return launch_status(launch_mxfp4_dequantize(codes, bscale, rows * (D / 32), dtype, out, (cudaStream_t)stream));
 }
 
+int mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_bscale, const uint8_t* b_codes, const uint8_t* b_bscale,
+                 int64_t M, int64_t N, int64_t K, int out_dtype, void* out, int* dev_status, cskv_stream_t stream) {
+  constexpr int64_t kMost = 1LL << 30;  // tile coordinates are 32-bit
+  if (M < 0 || N < 0 || K < 32 || K % 32 || M > kMost || N > kMost || K > kMost) return CSKV_ERR_INVALID_ARG;
+  int rc = check_value_dtype(out_dtype);
+  if (rc || M == 0 || N == 0) return rc;
+  if (!a_codes || !a_bscale || !b_codes || !b_bscale || !out) return CSKV_ERR_INVALID_ARG;
+  if (!aligned16(a_codes) || !aligned16(b_codes) || !aligned16(out)) return CSKV_ERR_INVALID_ARG;
+  int sms = 0;
+  rc = device_sms(&sms);
+  if (rc) return rc;
+  return launch_status(launch_mxfp4_matmul(a_codes, a_bscale, b_codes, b_bscale, M, N, K, out_dtype, out, sms,
+                                           dev_status, (cudaStream_t)stream));
+}
+
 // Sizes and pointers of kv_quantize_fp4 / kv_dequantize_fp4; 2^35 rows bound the grid.
 static int check_kv4(const void* rows, int dtype, int64_t n, const int64_t* list, int64_t cap, const void* cache) {
   if (n < 0 || n > (1LL << 35) || cap < 0 || (!list && cap < n)) return CSKV_ERR_INVALID_ARG;

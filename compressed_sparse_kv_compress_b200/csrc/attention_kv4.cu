@@ -25,7 +25,7 @@
 // too.  The roles' loops are kept short: unrolled ones missed the instruction cache.
 #include "attn_rows.cuh"
 #include "mx4.cuh"
-#include "sm100.cuh"
+#include "roles.cuh"
 
 namespace cskv {
 
@@ -41,7 +41,6 @@ constexpr uint32_t k4OffV = k4KStages * k4Half, k4OffRaw = k4OffV + k4VStages * 
 constexpr uint32_t k4Raw = k4Chunk * kKv4RowBytes;      // a chunk's rows as stored
 constexpr size_t k4Smem = k4OffRaw + k4RawStages * k4Raw + 1024;
 constexpr uint32_t k4ColO = 256, k4ColQ = 384;          // TMEM: S/P buffers at 0 and 128, O, Q
-constexpr long long k4WaitCycles = 1LL << 31;           // about a second: a wait gives up
 constexpr float k4Grow = 8.f;                           // log2: growth of the maximum that rescales
 
 struct K4Chunk {
@@ -62,24 +61,11 @@ struct K4Shared {
   uint64_t row[k4Table][k4Chunk];               // address of each row; 0: skipped
 };
 
-// Waits for phase `phase` of a barrier.  Bounded: one role that gives up makes every role of the
-// CTA leave its loop.  The waiting loop is one function for all sites, to keep their code short.
-__device__ __noinline__ bool k4_wait_slow(uint64_t* bar, uint32_t parity, int* abort, int* st) {
-  const long long t0 = clock64();
-  do {
-    if (mbar_poll(bar, parity)) return true;
-    if (*(volatile int*)abort) return false;
-  } while (clock64() - t0 < k4WaitCycles);
-  *(volatile int*)abort = 1;
-  flag(st, CSKV_DEV_TIMEOUT);
-  return false;
-}
 __device__ __forceinline__ bool k4_wait(K4Shared& sh, uint64_t* bar, uint32_t phase, int* st) {
-  return mbar_try_wait(bar, phase & 1u) || k4_wait_slow(bar, phase & 1u, &sh.abort, st);
+  return role_wait(bar, phase, &sh.abort, st);
 }
-// The same for a whole warp, whose lanes agree on the answer.
 __device__ __forceinline__ bool k4_wait_warp(K4Shared& sh, uint64_t* bar, uint32_t phase, int* st) {
-  return __all_sync(0xffffffffu, k4_wait(sh, bar, phase, st));
+  return role_wait_warp(bar, phase, &sh.abort, st);
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {

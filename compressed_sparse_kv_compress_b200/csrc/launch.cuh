@@ -176,6 +176,10 @@ cudaError_t launch_kv_quantize_fp4(const void* rows, int dtype, int64_t n, const
                                    uint8_t* out, int* st, cudaStream_t stream);
 cudaError_t launch_kv_dequantize_fp4(const uint8_t* cache, const int64_t* src, int64_t cap, int64_t n, int dtype,
                                      void* out, int* st, cudaStream_t stream);
+// mxfp4_matmul.cu
+cudaError_t launch_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scale, const uint8_t* b_codes,
+                                const uint8_t* b_scale, int64_t M, int64_t N, int64_t K, int out_dt, void* out,
+                                int sms, int* st, cudaStream_t stream);
 // staging.cu
 cudaError_t launch_copy_segments(const void* src, const int64_t* src_off, void* const* dst, const int64_t* len, int n,
                                  cudaStream_t stream);
