@@ -33,30 +33,34 @@ def _dt(t) -> int:
         raise ValueError(f"unsupported dtype {t.dtype}") from None
 
 
-def _check(fn: str, **tensors) -> None:
-    """Device and layout of the tensors handed to `fn` (None: not given): name=(tensor, dtypes,
-    shape), dtypes a dtype or a tuple of them, shape a tuple with None for a free extent.  All of
+def _check(fn: str, *specs) -> None:
+    """Refuses tensors that `fn` cannot take.  specs: (name, tensor or None, dtypes, shape); all of
     them have to be contiguous and on the current CUDA device, whose stream the call runs on."""
     dev = torch.cuda.current_device()
-    for name, (t, dts, shape) in tensors.items():
+    for name, t, dtypes, shape in specs:
         if t is None:
             continue
-        if t.device.type != "cuda" or t.device.index != dev:
+        if t.get_device() != dev:
             raise ValueError(f"{fn}: {name} is on {t.device}, not on the current device cuda:{dev}")
-        if t.dtype not in (dts if isinstance(dts, tuple) else (dts,)):
+        if t.dtype not in dtypes:
             raise ValueError(f"{fn}: {name} has dtype {t.dtype}")
-        if len(t.shape) != len(shape) or any(s is not None and s != g for s, g in zip(shape, t.shape)):
-            raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
+        if t.shape != shape:
+            raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{fn}: {name} is not contiguous")
 
 
+_U8 = (torch.uint8,)
+_I64 = (torch.int64,)
+_I32 = (torch.int32,)
 _VALUES = (torch.float32, torch.bfloat16)
 
 
 def _stream(stream) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle alone: building torch's stream object costs 3 us a call
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def csa_compress(x_a, z_a, x_b, z_b, tok_off, ent_off, out, *, max_blocks, bias_a=None, bias_b=None, tok0=None,
@@ -200,8 +204,9 @@ def hybrid_decode_attn(mode, q, kv_cmp, cmp_off, kv_raw, raw_off, q_seq, q_pos, 
         mode = int(mode) | ATTN_KV_FP8
     if kv_fp4:
         mode = int(mode) | ATTN_KV_FP4
-        _check("hybrid_decode_attn", q=(q, _VALUES, (T, H, d)), kv_cmp=(kv_cmp, torch.uint8, (None, KV4_ROW_BYTES)),
-               kv_raw=(kv_raw, q.dtype, (None, 256)), out=(out, _VALUES, (T, H, d)))
+        _check("hybrid_decode_attn", ("q", q, _VALUES, (T, H, d)),
+               ("kv_cmp", kv_cmp, _U8, (kv_cmp.shape[0], KV4_ROW_BYTES)),
+               ("kv_raw", kv_raw, (q.dtype,), (kv_raw.shape[0], 256)), ("out", out, _VALUES, (T, H, d)))
     if out.dtype == torch.bfloat16:
         mode = int(mode) | ATTN_OUT_BF16
     k = idx.shape[1] if idx is not None else 0
@@ -241,34 +246,40 @@ def kv_quantize_fp8(rows, out=None, stream=None):
     return out
 
 
+def _mxfp4_shapes(fn, lead, D):
+    """Shapes of the codes and scales of vectors [*lead, D]."""
+    if D < 1 or D % 32:
+        raise ValueError(f"{fn}: rows of {D} values; MXFP4 takes a multiple of 32")
+    return (*lead, D // 2), (*lead, D // 32)
+
+
 def mxfp4_quantize(x, codes=None, bscale=None, *, stream=None):
     """MXFP4 form of x [..., D] (fp32 or bf16, D a multiple of 32): (codes [..., D/2] uint8, two
     E2M1 codes a byte, bscale [..., D/32] uint8, one E8M0 scale per 32 values)."""
-    lead, D = tuple(x.shape[:-1]), int(x.shape[-1])
-    if D < 1 or D % 32:
-        raise ValueError(f"mxfp4_quantize: rows of {D} values; MXFP4 takes a multiple of 32")
+    *lead, D = x.shape
+    cs, bs = _mxfp4_shapes("mxfp4_quantize", lead, D)
     if codes is None:
-        codes = torch.empty(*lead, D // 2, dtype=torch.uint8, device=x.device)
+        codes = torch.empty(cs, dtype=torch.uint8, device=x.device)
     if bscale is None:
-        bscale = torch.empty(*lead, D // 32, dtype=torch.uint8, device=x.device)
-    _check("mxfp4_quantize", x=(x, _VALUES, lead + (D,)), codes=(codes, torch.uint8, lead + (D // 2,)),
-           bscale=(bscale, torch.uint8, lead + (D // 32,)))
-    st = _lib.load().mxfp4_quantize(_ptr(x), _dt(x), x.numel() // D, D, _ptr(codes), _ptr(bscale), _stream(stream))
+        bscale = torch.empty(bs, dtype=torch.uint8, device=x.device)
+    _check("mxfp4_quantize", ("x", x, _VALUES, x.shape), ("codes", codes, _U8, cs), ("bscale", bscale, _U8, bs))
+    st = _lib.load().mxfp4_quantize(x.data_ptr(), _DT[x.dtype], x.numel() // D, D, codes.data_ptr(),
+                                    bscale.data_ptr(), _stream(stream))
     _lib.check("mxfp4_quantize", st)
     return codes, bscale
 
 
 def mxfp4_dequantize(codes, bscale, out=None, *, dtype=torch.bfloat16, stream=None):
     """The values [..., D] of MXFP4 codes [..., D/2] with scales [..., D/32], as `dtype` (or out's)."""
-    lead, D = tuple(codes.shape[:-1]), 2 * int(codes.shape[-1])
-    if D < 1 or D % 32:
-        raise ValueError(f"mxfp4_dequantize: rows of {D} values; MXFP4 takes a multiple of 32")
+    *lead, half = codes.shape
+    D = 2 * half
+    _, bs = _mxfp4_shapes("mxfp4_dequantize", lead, D)
     if out is None:
-        out = torch.empty(*lead, D, dtype=dtype, device=codes.device)
-    _check("mxfp4_dequantize", codes=(codes, torch.uint8, lead + (D // 2,)),
-           bscale=(bscale, torch.uint8, lead + (D // 32,)), out=(out, _VALUES, lead + (D,)))
-    st = _lib.load().mxfp4_dequantize(_ptr(codes), _ptr(bscale), out.numel() // D, D, _dt(out), _ptr(out),
-                                      _stream(stream))
+        out = torch.empty((*lead, D), dtype=dtype, device=codes.device)
+    _check("mxfp4_dequantize", ("codes", codes, _U8, codes.shape), ("bscale", bscale, _U8, bs),
+           ("out", out, _VALUES, (*lead, D)))
+    st = _lib.load().mxfp4_dequantize(codes.data_ptr(), bscale.data_ptr(), out.numel() // D, D, _DT[out.dtype],
+                                      out.data_ptr(), _stream(stream))
     _lib.check("mxfp4_dequantize", st)
     return out
 
@@ -276,14 +287,14 @@ def mxfp4_dequantize(codes, bscale, out=None, *, dtype=torch.bfloat16, stream=No
 def mxfp4_matmul(a_codes, a_bscale, b_codes, b_bscale, out=None, *, dtype=torch.bfloat16, dev_status=None, stream=None):
     """out [M, N] = a b^T of MXFP4 matrices (mxfp4_quantize): a_codes [M, K/2], a_bscale [M, K/32],
     b_codes [N, K/2], b_bscale [N, K/32]; out fp32 or bf16 (`dtype`, or out's)."""
-    (M, half), N = a_codes.shape, int(b_codes.shape[0])
+    (M, half), (N, _) = a_codes.shape, b_codes.shape
     if out is None:
-        out = torch.empty(M, N, dtype=dtype, device=a_codes.device)
-    _check("mxfp4_matmul", a_codes=(a_codes, torch.uint8, (M, half)), a_bscale=(a_bscale, torch.uint8, (M, half // 16)),
-           b_codes=(b_codes, torch.uint8, (N, half)), b_bscale=(b_bscale, torch.uint8, (N, half // 16)),
-           out=(out, _VALUES, (M, N)), dev_status=(dev_status, torch.int32, (1,)))
-    st = _lib.load().mxfp4_matmul(_ptr(a_codes), _ptr(a_bscale), _ptr(b_codes), _ptr(b_bscale), M, N, 2 * half,
-                                  _dt(out), _ptr(out), _ptr(dev_status), _stream(stream))
+        out = torch.empty((M, N), dtype=dtype, device=a_codes.device)
+    _check("mxfp4_matmul", ("a_codes", a_codes, _U8, (M, half)), ("a_bscale", a_bscale, _U8, (M, half // 16)),
+           ("b_codes", b_codes, _U8, (N, half)), ("b_bscale", b_bscale, _U8, (N, half // 16)),
+           ("out", out, _VALUES, (M, N)), ("dev_status", dev_status, _I32, (1,)))
+    st = _lib.load().mxfp4_matmul(a_codes.data_ptr(), a_bscale.data_ptr(), b_codes.data_ptr(), b_bscale.data_ptr(),
+                                  M, N, 2 * half, _DT[out.dtype], out.data_ptr(), _ptr(dev_status), _stream(stream))
     _lib.check("mxfp4_matmul", st)
     return out
 
@@ -292,14 +303,15 @@ def kv_quantize_fp4(rows, out=None, *, dst=None, dev_status=None, stream=None):
     """4-bit main-KV rows ([cap, 176] uint8) from K||V rows [n, 256] (fp32 or bf16).  dst [n]
     int64: row i goes to out[dst[i]] (negative: left out; no two equal); None: to out[i].  Rows of
     `out` that are not named stay as they were."""
-    n = int(rows.shape[0])
+    n = rows.shape[0]
     if out is None:
         if dst is not None:
             raise ValueError("kv_quantize_fp4: dst needs the cache it points into (out)")
-        out = torch.empty(n, KV4_ROW_BYTES, dtype=torch.uint8, device=rows.device)
-    _check("kv_quantize_fp4", rows=(rows, _VALUES, (n, 256)), out=(out, torch.uint8, (None, KV4_ROW_BYTES)),
-           dst=(dst, torch.int64, (n,)), dev_status=(dev_status, torch.int32, (1,)))
-    st = _lib.load().kv_quantize_fp4(_ptr(rows), _dt(rows), n, _ptr(dst), int(out.shape[0]), _ptr(out),
+        out = torch.empty((n, KV4_ROW_BYTES), dtype=torch.uint8, device=rows.device)
+    cap = out.shape[0]
+    _check("kv_quantize_fp4", ("rows", rows, _VALUES, (n, 256)), ("out", out, _U8, (cap, KV4_ROW_BYTES)),
+           ("dst", dst, _I64, (n,)), ("dev_status", dev_status, _I32, (1,)))
+    st = _lib.load().kv_quantize_fp4(rows.data_ptr(), _DT[rows.dtype], n, _ptr(dst), cap, out.data_ptr(),
                                      _ptr(dev_status), _stream(stream))
     _lib.check("kv_quantize_fp4", st)
     return out
@@ -308,12 +320,13 @@ def kv_quantize_fp4(rows, out=None, *, dst=None, dev_status=None, stream=None):
 def kv_dequantize_fp4(cache, out=None, *, src=None, dtype=torch.bfloat16, dev_status=None, stream=None):
     """K||V values [n, 256] (`dtype`, or out's) of the 4-bit main-KV rows cache [cap, 176]: rows
     src [n] int64 of it (negative: zeros), or its first rows (all of them without `out`)."""
-    n = int(src.shape[0]) if src is not None else int(out.shape[0] if out is not None else cache.shape[0])
+    cap = cache.shape[0]
+    n = src.shape[0] if src is not None else out.shape[0] if out is not None else cap
     if out is None:
-        out = torch.empty(n, 256, dtype=dtype, device=cache.device)
-    _check("kv_dequantize_fp4", cache=(cache, torch.uint8, (None, KV4_ROW_BYTES)), out=(out, _VALUES, (n, 256)),
-           src=(src, torch.int64, (n,)), dev_status=(dev_status, torch.int32, (1,)))
-    st = _lib.load().kv_dequantize_fp4(_ptr(cache), _ptr(src), int(cache.shape[0]), n, _dt(out), _ptr(out),
+        out = torch.empty((n, 256), dtype=dtype, device=cache.device)
+    _check("kv_dequantize_fp4", ("cache", cache, _U8, (cap, KV4_ROW_BYTES)), ("out", out, _VALUES, (n, 256)),
+           ("src", src, _I64, (n,)), ("dev_status", dev_status, _I32, (1,)))
+    st = _lib.load().kv_dequantize_fp4(cache.data_ptr(), _ptr(src), cap, n, _DT[out.dtype], out.data_ptr(),
                                        _ptr(dev_status), _stream(stream))
     _lib.check("kv_dequantize_fp4", st)
     return out
