@@ -68,49 +68,6 @@ __device__ __forceinline__ bool k4_wait_warp(K4Shared& sh, uint64_t* bar, uint32
   return role_wait_warp(bar, phase, &sh.abort, st);
 }
 
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-  return d;
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-// 2^(e - 127) twice, as bf16 (2^-127 is a subnormal; 0xFF is NaN).
-__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t e) {
-  const uint32_t b = e == 0xFFu ? 0x7FC0u : e == 0 ? 0x0040u : e << 7;
-  return b * 0x00010001u;
-}
-// Four E2M1 codes (16 bits of w) -> two words of bf16 pairs: the high and low byte of each
-// magnitude come from 8-byte tables by byte permute; a selector nibble's top bit (the sign) turns
-// the selected 0x80 into 0xFF, whose low bit moves to the sign place.
-__device__ __forceinline__ void e2m1x4_bf16(uint32_t w, uint32_t wm, uint32_t s, uint32_t& o0, uint32_t& o1) {
-  const uint32_t hi = prmt(0x3F3F3F00u, 0x40404040u, wm), lo = prmt(0xC0800000u, 0xC0804000u, wm);
-  const uint32_t sg = prmt(0x80808080u, 0x80808080u, w);
-  const uint32_t hs = hi | ((sg << 7) & 0x80808080u);
-  o0 = mul_bf16x2(prmt(lo, hs, 0x5140u), s);
-  o1 = mul_bf16x2(prmt(lo, hs, 0x7362u), s);
-}
-__device__ __forceinline__ uint4 e2m1x8_bf16(uint32_t w, uint32_t s) {
-  uint4 o;
-  const uint32_t wm = w & 0x77777777u;
-  e2m1x4_bf16(w, wm, s, o.x, o.y);
-  e2m1x4_bf16(w >> 16, wm >> 16, s, o.z, o.w);
-  return o;
-}
-// Two E4M3 codes in the high bytes of h's halves -> bf16: exponent and mantissa moved into place
-// (value * 2^-120), then two exact products (one would overflow the factor for large scales).
-__device__ __forceinline__ uint32_t e4m3x2_bf16(uint32_t h, uint32_t s) {
-  const uint32_t b = ((h >> 4) & 0x07F007F0u) | (h & 0x80008000u);
-  return mul_bf16x2(mul_bf16x2(b, 0x7B807B80u), s);
-}
-__device__ __forceinline__ uint4 e4m3x8_bf16(uint32_t w0, uint32_t w1, uint32_t s) {
-  return make_uint4(e4m3x2_bf16(prmt(w0, 0u, 0x1404u), s), e4m3x2_bf16(prmt(w0, 0u, 0x3424u), s),
-                    e4m3x2_bf16(prmt(w1, 0u, 0x1404u), s), e4m3x2_bf16(prmt(w1, 0u, 0x3424u), s));
-}
-
 // Byte offset of 16-byte piece c (0..15 of 128 bf16 dims) of row r in a K or V buffer.
 __device__ __forceinline__ uint32_t k4_off(int r, int c) {
   return (uint32_t)(c >> 3) * k4Region + (uint32_t)r * 128 + ((uint32_t)((c & 7) ^ (r & 7)) << 4);

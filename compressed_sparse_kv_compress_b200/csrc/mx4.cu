@@ -15,20 +15,44 @@ constexpr int kMxUnroll = 4;                          // 256-value pieces of a w
 constexpr int kMxWarpValues = 256 * kMxUnroll;        // values a warp takes
 constexpr int kMxCtaValues = kMxWarpValues * (kMxThreads / 32);
 
-// Largest magnitude (as bits) of the four lanes that hold a block.
+// Largest magnitude (as bits; an infinity or a NaN stays the largest) of the four lanes that hold a
+// block.
 __device__ __forceinline__ uint32_t block_amax(const float (&x)[8]) {
-  uint32_t m = 0;
+  float a = fabsf(x[0]), b = fabsf(x[4]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  for (int i = 1; i < 4; ++i) a = amax_nan(a, x[i]), b = amax_nan(b, x[4 + i]);
+  uint32_t m = __float_as_uint(amax_nan(a, b));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
 
-// x * 2^(127 - e) for the conversion; in a block without a finite scale every code is zero.
+// x * 2^(127 - e) for the conversion.
 __device__ __forceinline__ void scale_down(float (&x)[8], uint32_t e) {
   const float inv = mx_inv_scale(e);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = e == 0xFFu ? 0.f : x[i] * inv;
+  for (int i = 0; i < 8; ++i) x[i] *= inv;
+}
+
+// Eight decoded values of a lane, stored: bf16 pairs straight from the codes, fp32 by value.
+__device__ __forceinline__ void store_e2m1x8(__nv_bfloat16* to, uint32_t w, uint32_t e) {
+  *reinterpret_cast<uint4*>(to) = e2m1x8_bf16(w, scale_bf16x2(e));
+}
+__device__ __forceinline__ void store_e2m1x8(float* to, uint32_t w, uint32_t e) {
+  const float s = mx_scale(e);
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = e2m1_value(w >> (4 * i)) * s;
+  Vec8<float>::store(to, f);
+}
+__device__ __forceinline__ void store_e4m3x8(__nv_bfloat16* to, uint32_t w0, uint32_t w1, uint32_t e) {
+  *reinterpret_cast<uint4*>(to) = e4m3x8_bf16(w0, w1, scale_bf16x2(e));
+}
+__device__ __forceinline__ void store_e4m3x8(float* to, uint32_t w0, uint32_t w1, uint32_t e) {
+  const float s = mx_scale(e);
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = e4m3_value((i < 4 ? w0 : w1) >> (8 * (i & 3))) * s;
+  Vec8<float>::store(to, f);
 }
 
 template <typename T>
@@ -55,7 +79,7 @@ __global__ void __launch_bounds__(kMxThreads) mxfp4_quantize_kernel(const T* __r
     scale_down(f[u], e);
     if ((lane & 3) == u) mine = e;
     if (b0 + 8 * u + (lane >> 2) < blocks)
-      *reinterpret_cast<uint32_t*>(codes + (b0 * kMxBlock + 256 * u + 8 * lane) / 2) = e2m1x8(f[u]);
+      *reinterpret_cast<uint32_t*>(codes + (b0 * kMxBlock + 256 * u + 8 * lane) / 2) = e == 0xFFu ? 0u : e2m1x8(f[u]);
   }
   // lane l keeps the scale of piece l % 4, block l / 4: a warp's 32 scale bytes in one store
   const int64_t b = b0 + 8 * (lane & 3) + (lane >> 2);
@@ -69,22 +93,17 @@ __global__ void __launch_bounds__(kMxThreads) mxfp4_dequantize_kernel(const uint
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t b0 = ((int64_t)blockIdx.x * kMxCtaValues + (threadIdx.x >> 5) * kMxWarpValues) / kMxBlock;
-  uint32_t w[kMxUnroll];
-  float s[kMxUnroll];
+  uint32_t w[kMxUnroll], e[kMxUnroll];
 #pragma unroll
   for (int u = 0; u < kMxUnroll; ++u) {
     const int64_t b = b0 + 8 * u + (lane >> 2);
     const bool ok = b < blocks;
     w[u] = ok ? __ldg(reinterpret_cast<const uint32_t*>(codes + (b0 * kMxBlock + 256 * u + 8 * lane) / 2)) : 0u;
-    s[u] = ok ? mx_scale(__ldg(scales + b)) : 0.f;
+    e[u] = ok ? __ldg(scales + b) : 0u;
   }
 #pragma unroll
-  for (int u = 0; u < kMxUnroll; ++u) {
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = e2m1_value(w[u] >> (4 * i)) * s[u];
-    if (b0 + 8 * u + (lane >> 2) < blocks) Vec8<T>::store(out + b0 * kMxBlock + 256 * u + 8 * lane, f);
-  }
+  for (int u = 0; u < kMxUnroll; ++u)
+    if (b0 + 8 * u + (lane >> 2) < blocks) store_e2m1x8(out + b0 * kMxBlock + 256 * u + 8 * lane, w[u], e[u]);
 }
 
 // ---------------------------------------------------------------- 4-bit main-KV rows
@@ -117,24 +136,20 @@ __global__ void __launch_bounds__(32 * kKv4Warps) kv_quantize_fp4_kernel(const T
   for (int u = 0; u < kKv4Rows; ++u) {
     const uint32_t e = mx_scale_code(block_amax(x[u]), rope ? kE4m3Emax : kE2m1Emax);
     scale_down(x[u], e);
-    // the eight scale bytes sit in lanes 0, 4, .. 28; lane 0 collects them
-    uint32_t lo = 0, hi = 0;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      lo |= __shfl_sync(0xffffffffu, e, 4 * b) << (8 * b);
-      hi |= __shfl_sync(0xffffffffu, e, 16 + 4 * b) << (8 * b);
-    }
     if (to[u] < 0) continue;
     if (to[u] >= cap) {
       if (lane == 0) flag(st, CSKV_DEV_BAD_INDEX);
       continue;
     }
     uint8_t* o = out + (size_t)to[u] * kKv4RowBytes;
-    if (rope)
-      *reinterpret_cast<uint2*>(o + kKv4Rope + 8 * (lane - 8)) = e4m3x8(x[u]);
-    else
-      *reinterpret_cast<uint32_t*>(o + (lane < 8 ? 4 * lane : kKv4V + 4 * (lane - 16))) = e2m1x8(x[u]);
-    if (lane == 0) *reinterpret_cast<uint4*>(o + kKv4Scales) = make_uint4(lo, hi, 0u, 0u);
+    if (rope) {
+      const uint2 w = e4m3x8(x[u]);
+      *reinterpret_cast<uint2*>(o + kKv4Rope + 8 * (lane - 8)) = e == 0xFFu ? make_uint2(0u, 0u) : w;
+    } else {
+      *reinterpret_cast<uint32_t*>(o + (lane < 8 ? 4 * lane : kKv4V + 4 * (lane - 16))) = e == 0xFFu ? 0u : e2m1x8(x[u]);
+    }
+    // a block's first lane stores its scale, its second one zero byte of the row's end
+    if ((lane & 3) < 2) o[kKv4Scales + (lane >> 2) + ((lane & 1) ? 8 : 0)] = (lane & 1) ? 0 : (uint8_t)e;
   }
 }
 
@@ -146,24 +161,32 @@ __global__ void __launch_bounds__(32 * kKv4Warps) kv_dequantize_fp4_kernel(const
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t r0 = ((int64_t)blockIdx.x * kKv4Warps + (threadIdx.x >> 5)) * kKv4Rows;
-  float x[kKv4Rows][8];
+  // all rows' loads go out before the first is decoded: a lane's codes are one word (RoPE: two)
+  const bool rope = lane >= 8 && lane < 16;
+  const int at = lane < 8 ? 4 * lane : rope ? kKv4Rope + 8 * (lane - 8) : kKv4V + 4 * (lane - 16);
+  uint32_t w0[kKv4Rows], w1[kKv4Rows], e[kKv4Rows];
 #pragma unroll
   for (int u = 0; u < kKv4Rows; ++u) {
     const int64_t r = r0 + u;
-    int64_t e = r >= n ? -1 : src ? __ldg(src + r) : r;
-    if (e >= cap) {
+    int64_t i = r >= n ? -1 : src ? __ldg(src + r) : r;
+    if (i >= cap) {
       if (lane == 0) flag(st, CSKV_DEV_BAD_INDEX);
-      e = -1;
+      i = -1;
     }
-    if (e >= 0)
-      kv4_load8(cache + (size_t)e * kKv4RowBytes, lane, x[u]);
-    else
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+    const uint8_t* row = cache + (size_t)(i < 0 ? 0 : i) * kKv4RowBytes;
+    w0[u] = i < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t*>(row + at));
+    w1[u] = i < 0 || !rope ? 0u : __ldg(reinterpret_cast<const uint32_t*>(row + at) + 1);
+    e[u] = i < 0 ? 127u : __ldg(row + kKv4Scales + (lane >> 2));
   }
 #pragma unroll
-  for (int u = 0; u < kKv4Rows; ++u)
-    if (r0 + u < n) Vec8<T>::store(out + (size_t)(r0 + u) * kRow + 8 * lane, x[u]);
+  for (int u = 0; u < kKv4Rows; ++u) {
+    if (r0 + u >= n) continue;
+    T* to = out + (size_t)(r0 + u) * kRow + 8 * lane;
+    if (rope)
+      store_e4m3x8(to, w0[u], w1[u], e[u]);
+    else
+      store_e2m1x8(to, w0[u], e[u]);
+  }
 }
 
 // ---------------------------------------------------------------- launchers

@@ -56,6 +56,27 @@ def test_vector_decode_covers_every_byte_and_scale():
     with np.errstate(over="ignore"):
         ref = codecs.mx_fp4_decode(c, bscale.cpu().numpy()).astype(np.float32).astype(np.float64)
     assert np.array_equal(out, ref, equal_nan=True)
+    # bf16: the exact value rounded once, at bf16's range (subnormals, infinity)
+    out16 = api.mxfp4_dequantize(codes, bscale)
+    with np.errstate(over="ignore"):
+        exact = torch.from_numpy(codecs.mx_fp4_decode(c, bscale.cpu().numpy()).astype(np.float32)).to(torch.bfloat16)
+    assert np.array_equal(to_f64(out16), to_f64(exact), equal_nan=True)
+
+
+def test_row_decode_covers_every_byte_and_scale():
+    """Rows with one scale code in all blocks and every byte value, decoded to both types."""
+    p = np.zeros((256, 176), dtype=np.uint8)
+    p[:, :160] = np.arange(160)[None]
+    p[128:, :160] = 96 + np.arange(160)[None]
+    e = np.concatenate([np.arange(0, 256, 2), np.arange(1, 256, 2)])
+    p[:, 160:168] = e[:, None]
+    rope = p[:, 32:96]
+    rope[(rope & 0x7F) == 0x7F] = 0                    # the quantiser writes no NaN code
+    cache = torch.from_numpy(p).cuda()
+    with np.errstate(over="ignore"):
+        ref = torch.from_numpy(kv4.decode_rows(p).astype(np.float32))
+    assert np.array_equal(to_f64(api.kv_dequantize_fp4(cache, dtype=torch.float32)), to_f64(ref), equal_nan=True)
+    assert np.array_equal(to_f64(api.kv_dequantize_fp4(cache)), to_f64(ref.to(torch.bfloat16)), equal_nan=True)
 
 
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
