@@ -107,10 +107,33 @@ __global__ void __launch_bounds__(kMxThreads) mxfp4_dequantize_kernel(const uint
 }
 
 // ---------------------------------------------------------------- 4-bit main-KV rows
-// A warp a row, a lane eight of its 256 values: lanes 0..7 and 16..31 hold E2M1 dims, 8..15 the
-// E4M3 RoPE dims.
+// A warp takes four rows as four groups of 32 lanes with eight values each: three groups are the
+// rows' 96 E2M1 pieces, one their 32 E4M3 pieces, so no lane waits for the other format's code
+// (with a row a warp both codes ran for every row, and the kernels were bound by issue: 41 and 44 us
+// for 262144 rows).
 constexpr int kKv4Warps = 8;
-constexpr int kKv4Rows = 4;  // rows of a warp in flight
+constexpr int kKv4Rows = 4;
+
+// Piece of a lane in group j: the row among the warp's four, and where its eight values, its codes
+// and its block's scale sit in a row.
+struct Kv4Piece {
+  int row, value, code, scale;
+};
+__device__ __forceinline__ Kv4Piece kv4_piece(int j, int lane) {
+  Kv4Piece p;
+  if (j < 3) {
+    const int i = lane + 32 * j, part = i % 24;  // K dims 0..63: 8 pieces, V: 16
+    p.row = i / 24;
+    p.value = 8 * part + (part < 8 ? 0 : 64);
+    p.code = part < 8 ? 4 * part : kKv4V + 4 * (part - 8);
+  } else {
+    p.row = lane >> 3;
+    p.value = 64 + 8 * (lane & 7);
+    p.code = kKv4Rope + 8 * (lane & 7);
+  }
+  p.scale = kKv4Scales + (p.value >> 5);
+  return p;
+}
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kKv4Warps) kv_quantize_fp4_kernel(const T* __restrict__ rows, int64_t n,
@@ -119,37 +142,38 @@ __global__ void __launch_bounds__(32 * kKv4Warps) kv_quantize_fp4_kernel(const T
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t r0 = ((int64_t)blockIdx.x * kKv4Warps + (threadIdx.x >> 5)) * kKv4Rows;
-  const bool rope = lane >= 8 && lane < 16;
-  float x[kKv4Rows][8];
-  int64_t to[kKv4Rows];
+  float x[4][8];
+  int64_t to[4];
 #pragma unroll
-  for (int u = 0; u < kKv4Rows; ++u) {
-    const int64_t r = r0 + u;
-    to[u] = r >= n ? -1 : dst ? __ldg(dst + r) : r;
+  for (int j = 0; j < 4; ++j) {
+    const Kv4Piece q = kv4_piece(j, lane);
+    const int64_t r = r0 + q.row;
+    to[j] = r >= n ? -1 : dst ? __ldg(dst + r) : r;
     if (r < n)
-      Vec8<T>::load(rows + (size_t)r * kRow + 8 * lane, x[u]);
+      Vec8<T>::load(rows + (size_t)r * kRow + q.value, x[j]);
     else
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+      for (int i = 0; i < 8; ++i) x[j][i] = 0.f;
   }
 #pragma unroll
-  for (int u = 0; u < kKv4Rows; ++u) {
-    const uint32_t e = mx_scale_code(block_amax(x[u]), rope ? kE4m3Emax : kE2m1Emax);
-    scale_down(x[u], e);
-    if (to[u] < 0) continue;
-    if (to[u] >= cap) {
-      if (lane == 0) flag(st, CSKV_DEV_BAD_INDEX);
+  for (int j = 0; j < 4; ++j) {
+    const Kv4Piece q = kv4_piece(j, lane);
+    const uint32_t e = mx_scale_code(block_amax(x[j]), j == 3 ? kE4m3Emax : kE2m1Emax);
+    scale_down(x[j], e);
+    if (to[j] < 0) continue;
+    if (to[j] >= cap) {
+      if (q.value == 64) flag(st, CSKV_DEV_BAD_INDEX);  // once a row
       continue;
     }
-    uint8_t* o = out + (size_t)to[u] * kKv4RowBytes;
-    if (rope) {
-      const uint2 w = e4m3x8(x[u]);
-      *reinterpret_cast<uint2*>(o + kKv4Rope + 8 * (lane - 8)) = e == 0xFFu ? make_uint2(0u, 0u) : w;
+    uint8_t* o = out + (size_t)to[j] * kKv4RowBytes;
+    if (j == 3) {
+      const uint2 w = e4m3x8(x[j]);
+      *reinterpret_cast<uint2*>(o + q.code) = e == 0xFFu ? make_uint2(0u, 0u) : w;
     } else {
-      *reinterpret_cast<uint32_t*>(o + (lane < 8 ? 4 * lane : kKv4V + 4 * (lane - 16))) = e == 0xFFu ? 0u : e2m1x8(x[u]);
+      *reinterpret_cast<uint32_t*>(o + q.code) = e == 0xFFu ? 0u : e2m1x8(x[j]);
     }
     // a block's first lane stores its scale, its second one zero byte of the row's end
-    if ((lane & 3) < 2) o[kKv4Scales + (lane >> 2) + ((lane & 1) ? 8 : 0)] = (lane & 1) ? 0 : (uint8_t)e;
+    if ((lane & 3) < 2) o[q.scale + ((lane & 1) ? 8 : 0)] = (lane & 1) ? 0 : (uint8_t)e;
   }
 }
 
@@ -161,31 +185,34 @@ __global__ void __launch_bounds__(32 * kKv4Warps) kv_dequantize_fp4_kernel(const
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t r0 = ((int64_t)blockIdx.x * kKv4Warps + (threadIdx.x >> 5)) * kKv4Rows;
-  // all rows' loads go out before the first is decoded: a lane's codes are one word (RoPE: two)
-  const bool rope = lane >= 8 && lane < 16;
-  const int at = lane < 8 ? 4 * lane : rope ? kKv4Rope + 8 * (lane - 8) : kKv4V + 4 * (lane - 16);
-  uint32_t w0[kKv4Rows], w1[kKv4Rows], e[kKv4Rows];
+  // all groups' loads go out before the first is decoded
+  uint2 w[4];
+  uint32_t e[4];
 #pragma unroll
-  for (int u = 0; u < kKv4Rows; ++u) {
-    const int64_t r = r0 + u;
+  for (int j = 0; j < 4; ++j) {
+    const Kv4Piece q = kv4_piece(j, lane);
+    const int64_t r = r0 + q.row;
     int64_t i = r >= n ? -1 : src ? __ldg(src + r) : r;
     if (i >= cap) {
-      if (lane == 0) flag(st, CSKV_DEV_BAD_INDEX);
+      if (q.value == 64) flag(st, CSKV_DEV_BAD_INDEX);  // once a row
       i = -1;
     }
     const uint8_t* row = cache + (size_t)(i < 0 ? 0 : i) * kKv4RowBytes;
-    w0[u] = i < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t*>(row + at));
-    w1[u] = i < 0 || !rope ? 0u : __ldg(reinterpret_cast<const uint32_t*>(row + at) + 1);
-    e[u] = i < 0 ? 127u : __ldg(row + kKv4Scales + (lane >> 2));
+    if (j == 3)
+      w[j] = i < 0 ? make_uint2(0u, 0u) : __ldg(reinterpret_cast<const uint2*>(row + q.code));
+    else
+      w[j] = make_uint2(i < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t*>(row + q.code)), 0u);
+    e[j] = i < 0 ? 127u : __ldg(row + q.scale);
   }
 #pragma unroll
-  for (int u = 0; u < kKv4Rows; ++u) {
-    if (r0 + u >= n) continue;
-    T* to = out + (size_t)(r0 + u) * kRow + 8 * lane;
-    if (rope)
-      store_e4m3x8(to, w0[u], w1[u], e[u]);
+  for (int j = 0; j < 4; ++j) {
+    const Kv4Piece q = kv4_piece(j, lane);
+    if (r0 + q.row >= n) continue;
+    T* to = out + (size_t)(r0 + q.row) * kRow + q.value;
+    if (j == 3)
+      store_e4m3x8(to, w[j].x, w[j].y, e[j]);
     else
-      store_e2m1x8(to, w0[u], e[u]);
+      store_e2m1x8(to, w[j].x, e[j]);
   }
 }
 
