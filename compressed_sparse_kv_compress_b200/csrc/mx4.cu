@@ -63,11 +63,14 @@ __global__ void __launch_bounds__(kMxThreads) mxfp4_quantize_kernel(const T* __r
   const int lane = threadIdx.x & 31;
   // first block of this warp; a lane's piece u is block b0 + 8u + lane/4, values 8 (lane % 4) ..
   const int64_t b0 = ((int64_t)blockIdx.x * kMxCtaValues + (threadIdx.x >> 5) * kMxWarpValues) / kMxBlock;
+  const T* from = x + b0 * kMxBlock + 8 * lane;
+  uint8_t* to = codes + b0 * (kMxBlock / 2) + 4 * lane;
+  const int left = (int)min((int64_t)(8 * kMxUnroll), blocks - b0) - (lane >> 2);  // blocks from this lane's first on
   float f[kMxUnroll][8];
 #pragma unroll
   for (int u = 0; u < kMxUnroll; ++u) {
-    if (b0 + 8 * u + (lane >> 2) < blocks)
-      Vec8<T>::load(x + b0 * kMxBlock + 256 * u + 8 * lane, f[u]);
+    if (left > 8 * u)
+      Vec8<T>::load(from + 256 * u, f[u]);
     else
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[u][i] = 0.f;
@@ -78,8 +81,7 @@ __global__ void __launch_bounds__(kMxThreads) mxfp4_quantize_kernel(const T* __r
     const uint32_t e = mx_scale_code(block_amax(f[u]), kE2m1Emax);
     scale_down(f[u], e);
     if ((lane & 3) == u) mine = e;
-    if (b0 + 8 * u + (lane >> 2) < blocks)
-      *reinterpret_cast<uint32_t*>(codes + (b0 * kMxBlock + 256 * u + 8 * lane) / 2) = e == 0xFFu ? 0u : e2m1x8(f[u]);
+    if (left > 8 * u) *reinterpret_cast<uint32_t*>(to + 128 * u) = e == 0xFFu ? 0u : e2m1x8(f[u]);
   }
   // lane l keeps the scale of piece l % 4, block l / 4: a warp's 32 scale bytes in one store
   const int64_t b = b0 + 8 * (lane & 3) + (lane >> 2);
@@ -93,17 +95,18 @@ __global__ void __launch_bounds__(kMxThreads) mxfp4_dequantize_kernel(const uint
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t b0 = ((int64_t)blockIdx.x * kMxCtaValues + (threadIdx.x >> 5) * kMxWarpValues) / kMxBlock;
+  const uint8_t *from = codes + b0 * (kMxBlock / 2) + 4 * lane, *sc = scales + b0 + (lane >> 2);
+  T* to = out + b0 * kMxBlock + 8 * lane;
+  const int left = (int)min((int64_t)(8 * kMxUnroll), blocks - b0) - (lane >> 2);  // blocks from this lane's first on
   uint32_t w[kMxUnroll], e[kMxUnroll];
 #pragma unroll
   for (int u = 0; u < kMxUnroll; ++u) {
-    const int64_t b = b0 + 8 * u + (lane >> 2);
-    const bool ok = b < blocks;
-    w[u] = ok ? __ldg(reinterpret_cast<const uint32_t*>(codes + (b0 * kMxBlock + 256 * u + 8 * lane) / 2)) : 0u;
-    e[u] = ok ? __ldg(scales + b) : 0u;
+    w[u] = left > 8 * u ? __ldg(reinterpret_cast<const uint32_t*>(from + 128 * u)) : 0u;
+    e[u] = left > 8 * u ? __ldg(sc + 8 * u) : 0u;
   }
 #pragma unroll
   for (int u = 0; u < kMxUnroll; ++u)
-    if (b0 + 8 * u + (lane >> 2) < blocks) store_e2m1x8(out + b0 * kMxBlock + 256 * u + 8 * lane, w[u], e[u]);
+    if (left > 8 * u) store_e2m1x8(to + 256 * u, w[u], e[u]);
 }
 
 // ---------------------------------------------------------------- 4-bit main-KV rows
@@ -142,18 +145,19 @@ __global__ void __launch_bounds__(32 * kKv4Warps) kv_quantize_fp4_kernel(const T
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t r0 = ((int64_t)blockIdx.x * kKv4Warps + (threadIdx.x >> 5)) * kKv4Rows;
+  if (r0 >= n) return;
+  const int here = (int)min((int64_t)kKv4Rows, n - r0);  // rows of this warp
+  const T* from = rows + (size_t)r0 * kRow;
   float x[4][8];
   int64_t to[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const Kv4Piece q = kv4_piece(j, lane);
-    const int64_t r = r0 + q.row;
-    to[j] = r >= n ? -1 : dst ? __ldg(dst + r) : r;
-    if (r < n)
-      Vec8<T>::load(rows + (size_t)r * kRow + q.value, x[j]);
-    else
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[j][i] = 0.f;
+    // past the end: the warp's first row again, not stored
+    const int row = q.row < here ? q.row : 0;
+    to[j] = dst ? __ldg(dst + r0 + row) : r0 + row;
+    Vec8<T>::load(from + (row * kRow + q.value), x[j]);
+    if (q.row >= here) to[j] = -1;
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -185,14 +189,15 @@ __global__ void __launch_bounds__(32 * kKv4Warps) kv_dequantize_fp4_kernel(const
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t r0 = ((int64_t)blockIdx.x * kKv4Warps + (threadIdx.x >> 5)) * kKv4Rows;
+  if (r0 >= n) return;
+  const int here = (int)min((int64_t)kKv4Rows, n - r0);  // rows of this warp
   // all groups' loads go out before the first is decoded
   uint2 w[4];
   uint32_t e[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const Kv4Piece q = kv4_piece(j, lane);
-    const int64_t r = r0 + q.row;
-    int64_t i = r >= n ? -1 : src ? __ldg(src + r) : r;
+    int64_t i = q.row >= here ? -1 : src ? __ldg(src + r0 + q.row) : r0 + q.row;
     if (i >= cap) {
       if (q.value == 64) flag(st, CSKV_DEV_BAD_INDEX);  // once a row
       i = -1;
@@ -207,8 +212,8 @@ __global__ void __launch_bounds__(32 * kKv4Warps) kv_dequantize_fp4_kernel(const
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const Kv4Piece q = kv4_piece(j, lane);
-    if (r0 + q.row >= n) continue;
-    T* to = out + (size_t)(r0 + q.row) * kRow + q.value;
+    if (q.row >= here) continue;
+    T* to = out + (size_t)r0 * kRow + (q.row * kRow + q.value);
     if (j == 3)
       store_e4m3x8(to, w[j].x, w[j].y, e[j]);
     else
