@@ -4,13 +4,15 @@
 // [SW] shareware.cn/news/167317 §六.1 (FP4 suffices for ranking): rows of E2M1 codes with one E8M0
 // scale per 32 values (mx4.cuh), exact products, fp32 accumulation.
 //
-// Large products are bound by the tensor pipe (and by shared memory, which feeds it 128 bytes a
-// cycle: a 128 x 192 tile needs 106), a few rows by the bytes of b.  A persistent CTA an SM, with
-// roles: one thread loads code tiles by TMA (128-byte swizzle, 256 codes deep, zeros past the edges),
-// four warps load the rows' scales and lay them out as the tensor core wants them, one thread
-// copies scales to tensor memory and issues the products, four warps write out the tile before
-// last (two accumulators).  The 128-row operand is a, or, for a few rows of a, b: the tile is then
-// as narrow as those rows.
+// Large products are bound by what L2 delivers to the SMs (128 x 192 tiles: 41 KB a step, 7.8 TB/s
+// measured; the tensor pipe would take a quarter of that time), so they take 256 x 192 tiles, two
+// products a loaded tile of the other operand; a few rows are bound by the bytes of b and the
+// latency of a step, so few tiles are split over the inner length inside a thread-block cluster.
+// A persistent CTA an SM, with roles: one thread loads code tiles by TMA (128-byte swizzle, 256
+// codes deep, zeros past the edges), four warps load the rows' scales and lay them out as the
+// tensor core wants them, one thread copies scales to tensor memory and issues the products, four
+// or eight warps write out the tile (of 128 rows: while the next one's products run).  The 128-row
+// operand P is a, or, for a few rows of a, b: the tile is then as narrow as those rows.
 #include <cuda.h>
 
 #include "launch.cuh"
@@ -18,11 +20,12 @@
 
 namespace cskv {
 
-constexpr int kMmThreads = 320;          // warp 0 TMA, 1 products, 2-5 scales, 6-9 output
-constexpr int kMmScaleWarps = 4;
+constexpr int kMmThreads = 448;          // warp 0 TMA, 1 products, 2-5 scales, 6-13 output
+constexpr int kMmScaleWarps = 4, kMmOutWarp = 2 + kMmScaleWarps;
 constexpr int kMmDeep = 256;             // codes of a stage: 128 bytes a row
-constexpr uint32_t kMmTileP = 128 * 128;  // bytes of the 128-row operand's tile
+constexpr uint32_t kMmTileP = 128 * 128;  // bytes of 128 rows' codes
 constexpr int kMmSfStep = 32;            // TMEM columns of one stage's scales
+constexpr int kMmMaxSplit = 8;           // CTAs of a cluster that share a tile's inner length
 
 struct MmParams {
   CUtensorMap p_map, q_map;  // codes of the 128-row operand P and of the other, Q
@@ -30,24 +33,28 @@ struct MmParams {
   int64_t p_rows, q_rows, k32;  // k32: scale bytes of a row
   int64_t ld;                   // N
   int p_tiles, q_tiles, steps;
+  int split;                    // CTAs that share a tile (the size of the cluster)
   int p_is_a;                   // out[p, q] (P rows are a's), else out[q, p]
-  int wide;                     // scale rows are whole 4-byte words
+  int wide;                     // bytes of a scale load: 8, 4 or 1
   void* out;
   int* st;
 };
 
-template <int NQ>
+// MT x 128 rows of P by NQ of Q.
+template <int MT, int NQ>
 struct MmShape {
-  static constexpr int qc = (NQ + 127) / 128;               // 128-row scale chunks of Q
-  static constexpr uint32_t codes = kMmTileP + NQ * 128u;   // a stage's code bytes
-  static constexpr uint32_t scales = 1024u * (1 + qc);      // two K chunks each
+  static constexpr int qc = (NQ + 127) / 128;                    // 128-row scale chunks of Q
+  static constexpr uint32_t codes = MT * kMmTileP + NQ * 128u;   // a stage's code bytes
+  static constexpr uint32_t scales = 1024u * (MT + qc);          // two K chunks each
   static constexpr uint32_t stage = (codes + scales + 1023u) / 1024u * 1024u;
   static constexpr int stages = (int)(196608u / stage) < 8 ? (int)(196608u / stage) : 8;
   static constexpr size_t smem = (size_t)stage * stages + 1024;
-  static constexpr int acc_cols = NQ < 32 ? 32 : NQ;        // TMEM columns of an accumulator
+  static constexpr int acc_cols = NQ < 32 ? 32 : NQ;             // TMEM columns of 128 rows' accumulator
+  static constexpr int accs = MT == 1 ? 2 : 1;                   // tiles in tensor memory
   static constexpr int sf_col = 2 * acc_cols;
   static constexpr int cols = sf_col + 2 * kMmSfStep <= 128 ? 128 : sf_col + 2 * kMmSfStep <= 256 ? 256 : 512;
-  static_assert(sf_col + 2 * kMmSfStep <= 512 && 8 * (1 + qc) <= kMmSfStep, "tensor memory");
+  static_assert(sf_col + 2 * kMmSfStep <= 512 && 8 * (MT + qc) <= kMmSfStep, "tensor memory");
+  static_assert((size_t)stage * stages >= 128u * NQ * 4u, "a split tile's partial fits the ring");
 };
 
 struct MmShared {
@@ -59,34 +66,80 @@ struct MmShared {
 // Scale bytes 8 step .. 8 step + 7 of a row, zeros past its end or for a row that is not there.
 __device__ __forceinline__ uint2 mm_scales(const uint8_t* scale, int64_t row, int64_t rows, int64_t k32, int step,
                                            int wide) {
-  uint32_t w[2] = {0u, 0u};
+  uint2 w = make_uint2(0u, 0u);
   if (row < rows) {
     const uint8_t* s = scale + row * k32 + 8 * (int64_t)step;
     const int left = (int)min((int64_t)8, k32 - 8 * (int64_t)step);
-    if (wide) {
-      w[0] = __ldg(reinterpret_cast<const uint32_t*>(s));
-      if (left > 4) w[1] = __ldg(reinterpret_cast<const uint32_t*>(s) + 1);
+    if (wide == 8) {
+      w = __ldg(reinterpret_cast<const uint2*>(s));
+    } else if (wide == 4) {
+      w.x = __ldg(reinterpret_cast<const uint32_t*>(s));
+      if (left > 4) w.y = __ldg(reinterpret_cast<const uint32_t*>(s) + 1);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < left) w[i >> 2] |= (uint32_t)__ldg(s + i) << (8 * (i & 3));
+        if (i < left) (i < 4 ? w.x : w.y) |= (uint32_t)__ldg(s + i) << (8 * (i & 3));
     }
   }
-  return make_uint2(w[0], w[1]);
+  return w;
 }
 
-template <int NQ, typename T>
+// Columns q .. q + STEP - 1 of row `pr` of a tile.
+template <int STEP, typename T>
+__device__ __forceinline__ void mm_store(const MmParams& p, int64_t pr, int64_t q, const float (&v)[STEP]) {
+  if (pr >= p.p_rows || q >= p.q_rows) return;
+  T* out = reinterpret_cast<T*>(p.out);
+  auto one = [](float x) {
+    if constexpr (sizeof(T) == 2)
+      return __float2bfloat16_rn(x);
+    else
+      return x;
+  };
+  const bool whole = q + STEP <= p.q_rows;
+  if (!p.p_is_a) {  // out[q, p]: neighbouring lanes on neighbouring columns
+#pragma unroll
+    for (int i = 0; i < STEP; ++i)
+      if (whole || q + i < p.q_rows) out[(q + i) * p.ld + pr] = one(v[i]);
+    return;
+  }
+  T* dst = out + pr * p.ld + q;
+  if constexpr (STEP % 8 == 0) {
+    if (whole && (p.ld * sizeof(T)) % 16 == 0) {  // rows of out, and q's multiples of 8, are 16-byte places
+#pragma unroll
+      for (int i = 0; i < STEP; i += 8) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = v[i + j];
+        Vec8<T>::store(dst + i, f);
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < STEP; ++i)
+    if (whole || q + i < p.q_rows) dst[i] = one(v[i]);
+}
+
+template <int MT, int NQ, typename T>
 __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __grid_constant__ MmParams p) {
-  using Sh = MmShape<NQ>;
+  using Sh = MmShape<MT, NQ>;
   extern __shared__ __align__(1024) uint8_t smraw[];
   uint8_t* buf = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~(uintptr_t)1023);
   __shared__ MmShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t tiles = (int64_t)p.p_tiles * p.q_tiles;
+  // this CTA's part of its tiles' inner length
+  const int split = p.split, rank = split > 1 ? (int)cluster_rank() : 0;
+  const int64_t tile0 = blockIdx.x / split, stride = gridDim.x / split;
+  const int k0 = (int)((int64_t)p.steps * rank / split), k1 = (int)((int64_t)p.steps * (rank + 1) / split);
 
   if (warp == 1) {
     tmem_alloc(&sh.tmem, Sh::cols);
     tmem_relinquish();
+  }
+  if (tid == 32 * kMmOutWarp) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&p.p_map) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&p.q_map) : "memory");
   }
   if (tid == 0) {
     for (int i = 0; i < Sh::stages; ++i) {
@@ -96,7 +149,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.acc_full[i], 1);
-      mbar_init(&sh.acc_empty[i], 4);
+      mbar_init(&sh.acc_empty[i], 4 * MT);
     }
     mbar_init(&sh.bail, 1);
     sh.abort = 0;
@@ -114,16 +167,16 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
     if (lane == 0) {
       uint32_t g = 0;
       bool ok = true;
-      for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      for (int64_t tile = tile0; tile < tiles && ok; tile += stride) {
         const int pt = (int)(tile % p.p_tiles), qt = (int)(tile / p.p_tiles);
-        for (int k = 0; k < p.steps && ok; ++k, ++g) {
+        for (int k = k0; k < k1 && ok; ++k, ++g) {
           const uint32_t s = g % Sh::stages;
           if (g >= Sh::stages) ok = role_wait(&sh.empty[s], g / Sh::stages - 1, &sh.abort, p.st);
           if (!ok) break;
           uint8_t* dst = buf + s * Sh::stage;
           mbar_arrive_expect_tx(&sh.full[s], Sh::codes);
-          tma_load_2d(dst, &p.p_map, k * 128, pt * 128, &sh.full[s]);
-          tma_load_2d(dst + kMmTileP, &p.q_map, k * 128, qt * NQ, &sh.full[s]);
+          tma_load_2d(dst, &p.p_map, k * 128, pt * (MT * 128), &sh.full[s]);
+          tma_load_2d(dst + MT * kMmTileP, &p.q_map, k * 128, qt * NQ, &sh.full[s]);
         }
       }
       // the last loads have landed before this CTA's memory is released
@@ -137,28 +190,33 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
       const uint32_t base = smem_u32(buf);
       uint32_t g = 0, n = 0;
       bool ok = true;
-      for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++n) {
-        if (n >= 2) ok = role_wait(&sh.acc_empty[n & 1], n / 2 - 1, &sh.abort, p.st);
+      for (int64_t tile = tile0; tile < tiles && ok; tile += stride, ++n) {
+        const uint32_t ab = n % Sh::accs;
+        if (n >= Sh::accs) ok = role_wait(&sh.acc_empty[ab], n / Sh::accs - 1, &sh.abort, p.st);
         tc_fence_after();
-        for (int k = 0; k < p.steps && ok; ++k, ++g) {
+        for (int k = k0; k < k1 && ok; ++k, ++g) {
           const uint32_t s = g % Sh::stages, at = base + s * Sh::stage, sf = at + Sh::codes;
           ok = role_wait(&sh.full[s], g / Sh::stages, &sh.abort, p.st) &&
                role_wait(&sh.sf_full[s], g / Sh::stages, &sh.abort, p.st);
           if (!ok) break;
           tc_fence_after();
-          // scales: chunk c of P (K chunk c), then of Q (K chunk c, 128 rows each)
+          // scales, 512 bytes a chunk of 128 rows and 4 K scales: P's subtiles (two K chunks each), then
+          // Q's rows by K chunk
           const uint32_t col = tmem + Sh::sf_col + (g & 1) * kMmSfStep;
 #pragma unroll
-          for (int c = 0; c < 2 * (1 + Sh::qc); ++c)
+          for (int c = 0; c < 2 * (MT + Sh::qc); ++c)
             tc_cp_scales(col + 4 * c, smem_desc_noswz(sf + 512 * c, 16, 128));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_mxf4(tmem + (n & 1) * Sh::acc_cols, smem_desc_sw128(at + 32 * kk, 16, 1024),
-                        smem_desc_sw128(at + kMmTileP + 32 * kk, 16, 1024), idesc_mxf4(128, NQ, 2 * (kk & 1)),
-                        col + 4 * (kk >> 1), col + 8 + 4 * Sh::qc * (kk >> 1), k > 0 || kk > 0);
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_mxf4(tmem + (MT == 1 ? ab : mt) * Sh::acc_cols,
+                          smem_desc_sw128(at + mt * kMmTileP + 32 * kk, 16, 1024),
+                          smem_desc_sw128(at + MT * kMmTileP + 32 * kk, 16, 1024), idesc_mxf4(128, NQ, 2 * (kk & 1)),
+                          col + 8 * mt + 4 * (kk >> 1), col + 8 * MT + 4 * Sh::qc * (kk >> 1), k > k0 || kk > 0);
           tc_commit(&sh.empty[s]);
         }
-        if (ok) tc_commit(&sh.acc_full[n & 1]);
+        if (ok) tc_commit(&sh.acc_full[ab]);
       }
       if (!ok) {  // gave up: nothing of this CTA may still be in flight when its memory is released
         tc_commit(&sh.bail);
@@ -166,24 +224,26 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
       }
     }
     __syncwarp();
-  } else if (warp < 2 + kMmScaleWarps) {
+  } else if (warp < kMmOutWarp) {
     // ---------------------------------------------------------------- scales
-    // Warp w takes every fourth step.  A row's eight bytes are two words, one for each 512-byte
+    // Warp w takes every fourth step (with three stages every third, by three warps: a warp must not
+    // run past a release of a stage that it has not seen).  A row's eight bytes are two words, one for each 512-byte
     // chunk of 128 rows x 4 K scales: row r at 16 (r % 32) + 4 (r / 32).
-    constexpr int kRows = (128 + NQ + 31) / 32;
+    constexpr int kWarps = Sh::stages < kMmScaleWarps ? Sh::stages : kMmScaleWarps;
+    constexpr int kP = 128 * MT, kRows = (kP + NQ + 31) / 32;
     uint32_t g = 0;
     bool ok = true;
-    for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-      const int64_t p0 = (tile % p.p_tiles) * 128, q0 = (tile / p.p_tiles) * NQ;
-      for (int k = 0; k < p.steps && ok; ++k, ++g) {
-        if ((int)(g % kMmScaleWarps) != warp - 2) continue;
+    for (int64_t tile = tile0; tile < tiles && ok; tile += stride) {
+      const int64_t p0 = (tile % p.p_tiles) * kP, q0 = (tile / p.p_tiles) * NQ;
+      for (int k = k0; k < k1 && ok; ++k, ++g) {
+        if ((int)(g % kWarps) != warp - 2) continue;
         uint2 w[kRows];
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
           const int r = lane + 32 * i;
-          w[i] = r < 128      ? mm_scales(p.p_scale, p0 + r, p.p_rows, p.k32, k, p.wide)
-                 : r < 128 + NQ ? mm_scales(p.q_scale, q0 + r - 128, p.q_rows, p.k32, k, p.wide)
-                                : make_uint2(0u, 0u);
+          w[i] = r < kP      ? mm_scales(p.p_scale, p0 + r, p.p_rows, p.k32, k, p.wide)
+                 : r < kP + NQ ? mm_scales(p.q_scale, q0 + r - kP, p.q_rows, p.k32, k, p.wide)
+                               : make_uint2(0u, 0u);
         }
         const uint32_t s = g % Sh::stages;
         if (g >= Sh::stages) ok = role_wait_warp(&sh.empty[s], g / Sh::stages - 1, &sh.abort, p.st);
@@ -191,13 +251,12 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
         uint8_t* sf = buf + s * Sh::stage + Sh::codes;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-          const int r = lane + 32 * i;
-          const int q = r - 128;
-          uint8_t* to = r < 128 ? sf + 16 * (r & 31) + 4 * (r >> 5)
-                                : sf + 1024 + 512 * (q >> 7) + 16 * (q & 31) + 4 * ((q & 127) >> 5);
-          if (r < 128 + NQ) {
+          const int r = lane + 32 * i, q = r - kP;
+          uint8_t* to = r < kP ? sf + 1024 * (r >> 7) + 16 * (r & 31) + 4 * ((r & 127) >> 5)
+                               : sf + 1024 * MT + 512 * (q >> 7) + 16 * (q & 31) + 4 * ((q & 127) >> 5);
+          if (r < kP + NQ) {
             *reinterpret_cast<uint32_t*>(to) = w[i].x;
-            *reinterpret_cast<uint32_t*>(to + (r < 128 ? 512 : 512 * Sh::qc)) = w[i].y;
+            *reinterpret_cast<uint32_t*>(to + (r < kP ? 512 : 512 * Sh::qc)) = w[i].y;
           }
         }
         fence_proxy_async_smem();
@@ -207,66 +266,66 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
     }
   } else {
     // ---------------------------------------------------------------- output
-    const int quad = warp & 3;  // the TMEM lanes this warp may read
-    const int64_t row_in = quad * 32 + lane;
+    // Eight warps: the first four write 128 rows, the others the second 128 of a 256-row tile.  A
+    // split tile's partial goes to shared memory instead ([column][row]; the ring is done with).
+    const int quad = warp & 3, mt = (warp - kMmOutWarp) >> 2;  // the TMEM lanes this warp may read
+    const int row_in = quad * 32 + lane;
     constexpr int kStep = NQ < 32 ? 16 : 32;
-    const bool vec = (p.ld * sizeof(T)) % 16 == 0;  // rows of out start on 16-byte boundaries
-    T* out = reinterpret_cast<T*>(p.out);
     uint32_t n = 0;
-    bool ok = true;
-    for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++n) {
-      const int64_t pr = (tile % p.p_tiles) * 128 + row_in, q0 = (tile / p.p_tiles) * NQ;
-      ok = role_wait_warp(&sh.acc_full[n & 1], n / 2, &sh.abort, p.st);
+    bool ok = mt < MT;
+    for (int64_t tile = tile0; tile < tiles && ok; tile += stride, ++n) {
+      const int64_t pr = (tile % p.p_tiles) * (MT * 128) + mt * 128 + row_in, q0 = (tile / p.p_tiles) * NQ;
+      const uint32_t ab = n % Sh::accs;
+      ok = role_wait_warp(&sh.acc_full[ab], n / Sh::accs, &sh.abort, p.st);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t acc = tmem + (n & 1) * Sh::acc_cols + ((uint32_t)(quad * 32) << 16);
+      const uint32_t acc = tmem + (MT == 1 ? ab : mt) * Sh::acc_cols + ((uint32_t)(quad * 32) << 16);
 #pragma unroll 1
       for (int c = 0; c < NQ; c += kStep) {
-        uint32_t v[32];
+        uint32_t v[kStep];
         __syncwarp();
-        if constexpr (kStep == 16) {
-          uint32_t x[16];
-          tmem_ld16(acc + c, x);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = x[i];
-        } else {
+        if constexpr (kStep == 16)
+          tmem_ld16(acc + c, v);
+        else
           tmem_ld32(acc + c, v);
-        }
         tmem_ld_wait();
-        const int64_t q = q0 + c;
-        if (pr >= p.p_rows || q >= p.q_rows) continue;
-        if (!p.p_is_a) {  // out[q, p]: neighbouring lanes on neighbouring columns
+        float f[kStep];
 #pragma unroll
-          for (int i = 0; i < kStep; ++i)
-            if (q + i < p.q_rows) {
-              if constexpr (sizeof(T) == 2)
-                out[(q + i) * p.ld + pr] = __float2bfloat16_rn(__uint_as_float(v[i]));
-              else
-                out[(q + i) * p.ld + pr] = __uint_as_float(v[i]);
-            }
-        } else if (vec && q + kStep <= p.q_rows) {
-          T* dst = out + pr * p.ld + q;
-#pragma unroll
-          for (int i = 0; i < kStep; i += 8) {
-            float f[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(v[i + j]);
-            Vec8<T>::store(dst + i, f);
-          }
+        for (int i = 0; i < kStep; ++i) f[i] = __uint_as_float(v[i]);
+        if (split == 1) {
+          mm_store<kStep, T>(p, pr, q0 + c, f);
         } else {
 #pragma unroll
-          for (int i = 0; i < kStep; ++i)
-            if (q + i < p.q_rows) {
-              if constexpr (sizeof(T) == 2)
-                out[pr * p.ld + q + i] = __float2bfloat16_rn(__uint_as_float(v[i]));
-              else
-                out[pr * p.ld + q + i] = __uint_as_float(v[i]);
-            }
+          for (int i = 0; i < kStep; ++i) reinterpret_cast<float*>(buf)[(c + i) * 128 + row_in] = f[i];
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.acc_empty[n & 1]);
+      if (lane == 0) mbar_arrive(&sh.acc_empty[ab]);
+    }
+  }
+  if (split > 1) {
+    // ---------------------------------------------------------------- a split tile's sum
+    // Each CTA adds up its share of the columns over the cluster, in rank order.
+    if constexpr (MT == 1) {
+      __syncwarp();
+      cluster_sync();
+      if (warp >= kMmOutWarp && warp < kMmOutWarp + 4) {
+        const int row_in = (warp - kMmOutWarp) * 32 + lane;
+        const int64_t pr = (tile0 % p.p_tiles) * 128 + row_in, q0 = (tile0 / p.p_tiles) * NQ;
+        const int c0 = NQ * rank / split, c1 = NQ * (rank + 1) / split;
+        for (int c = c0; c < c1; c += 2) {  // NQ / split is 2 at least
+          float f[2] = {0.f, 0.f};
+#pragma unroll
+          for (int r = 0; r < kMmMaxSplit; ++r)
+            if (r < split) {
+              f[0] += ld_cluster_f32(smem_u32(buf) + (c * 128 + row_in) * 4, r);
+              f[1] += ld_cluster_f32(smem_u32(buf) + ((c + 1) * 128 + row_in) * 4, r);
+            }
+          mm_store<2, T>(p, pr, q0 + c, f);
+        }
+      }
+      cluster_sync();  // the others may still read this CTA's partial
     }
   }
   pdl_launch_dependents();
@@ -310,22 +369,45 @@ static bool mm_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NQ, typename T>
+template <int MT, int NQ, typename T>
 static cudaError_t mm_launch_as(const MmParams& p, int sms, cudaStream_t stream) {
-  auto kern = mxfp4_matmul_kernel<NQ, T>;
-  cudaError_t e = ensure_smem(kern, MmShape<NQ>::smem);
+  auto kern = mxfp4_matmul_kernel<MT, NQ, T>;
+  cudaError_t e = ensure_smem(kern, MmShape<MT, NQ>::smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)p.p_tiles * p.q_tiles;
-  e = launch_dependent(kern, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kMmThreads), MmShape<NQ>::smem, stream, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.split > 1 ? tiles * p.split : tiles < sms ? tiles : sms));
+  cfg.blockDim = dim3(kMmThreads);
+  cfg.dynamicSmemBytes = MmShape<MT, NQ>::smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.split > 1 ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kern, p);
   note_launch();
   return e;
 }
 
-template <int NQ>
-static cudaError_t mm_launch(MmParams& p, const uint8_t* q_codes, int64_t K, int out_dt, int sms, cudaStream_t stream) {
+template <int MT, int NQ>
+static cudaError_t mm_launch(MmParams& p, const uint8_t* p_codes, const uint8_t* q_codes, int64_t K, int out_dt,
+                             int sms, cudaStream_t stream) {
+  p.p_tiles = (int)((p.p_rows + MT * 128 - 1) / (MT * 128));
   p.q_tiles = (int)((p.q_rows + NQ - 1) / NQ);
-  if (!mm_map(&p.q_map, q_codes, p.q_rows, K, NQ)) return cudaErrorNotSupported;
-  return out_dt == CSKV_F32 ? mm_launch_as<NQ, float>(p, sms, stream) : mm_launch_as<NQ, __nv_bfloat16>(p, sms, stream);
+  // few tiles: their inner length is split over a cluster, two steps a CTA at least
+  p.split = 1;
+  if (MT == 1 && NQ <= 64)
+    while (p.split < kMmMaxSplit && (int64_t)p.p_tiles * p.q_tiles * p.split * 2 <= sms && p.steps >= 4 * p.split)
+      p.split *= 2;
+  if (!mm_map(&p.p_map, p_codes, p.p_rows, K, MT * 128) || !mm_map(&p.q_map, q_codes, p.q_rows, K, NQ))
+    return cudaErrorNotSupported;
+  return out_dt == CSKV_F32 ? mm_launch_as<MT, NQ, float>(p, sms, stream)
+                            : mm_launch_as<MT, NQ, __nv_bfloat16>(p, sms, stream);
 }
 
 cudaError_t launch_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scale, const uint8_t* b_codes,
@@ -342,27 +424,30 @@ cudaError_t launch_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scale, 
   p.k32 = K / 32;
   p.ld = N;
   p.steps = (int)((K + kMmDeep - 1) / kMmDeep);
-  p.wide = p.k32 % 4 == 0 && (((uintptr_t)a_scale | (uintptr_t)b_scale) & 3u) == 0;
+  const uintptr_t places = (uintptr_t)a_scale | (uintptr_t)b_scale | (uintptr_t)p.k32;
+  p.wide = places % 8 == 0 ? 8 : places % 4 == 0 ? 4 : 1;
   p.out = out;
   p.st = st;
-  p.p_tiles = (int)((p.p_rows + 127) / 128);
-  if (!mm_map(&p.p_map, pc, p.p_rows, K, 128)) return cudaErrorNotSupported;
   if (!p.p_is_a)
-    return M <= 16 ? mm_launch<16>(p, qc, K, out_dt, sms, stream)
-           : M <= 32 ? mm_launch<32>(p, qc, K, out_dt, sms, stream)
-                     : mm_launch<64>(p, qc, K, out_dt, sms, stream);
-  // the width whose waves of tiles take the fewest column steps (a tile costs its columns and a
-  // fixed part, about 32 columns' worth)
-  int best = 192;
-  int64_t cost = INT64_MAX;
-  for (int nq : {192, 128, 64}) {
-    const int64_t tiles = (int64_t)p.p_tiles * ((p.q_rows + nq - 1) / nq);
-    const int64_t c = (tiles + sms - 1) / sms * (nq + 32);
-    if (c < cost) cost = c, best = nq;
+    return M <= 16 ? mm_launch<1, 16>(p, pc, qc, K, out_dt, sms, stream)
+           : M <= 32 ? mm_launch<1, 32>(p, pc, qc, K, out_dt, sms, stream)
+                     : mm_launch<1, 64>(p, pc, qc, K, out_dt, sms, stream);
+  // The tile whose waves take the least time, in SM cycles: a step brings a tile's rows (128 bytes
+  // each, at the 28 bytes a cycle that L2 delivers to every SM at once), a tile costs about 400
+  // cycles more, and 10 a column where its output is not hidden (256 rows).
+  int best = 0;
+  int64_t least = INT64_MAX;
+  for (int nq : {2 * 1000 + 192, 192, 128, 64}) {
+    const int mt = nq / 1000 + (nq < 1000), cols = nq % 1000;
+    const int64_t tiles = ((p.p_rows + 128 * mt - 1) / (128 * mt)) * ((p.q_rows + cols - 1) / cols);
+    const int64_t cost = (tiles + sms - 1) / sms *
+                         (p.steps * (int64_t)((128 * mt + cols) * 128 / 28) + 400 + (mt == 2 ? 10 * cols : 0));
+    if (cost < least) least = cost, best = nq;
   }
-  return best == 192 ? mm_launch<192>(p, qc, K, out_dt, sms, stream)
-         : best == 128 ? mm_launch<128>(p, qc, K, out_dt, sms, stream)
-                       : mm_launch<64>(p, qc, K, out_dt, sms, stream);
+  return best == 2192  ? mm_launch<2, 192>(p, pc, qc, K, out_dt, sms, stream)
+         : best == 192 ? mm_launch<1, 192>(p, pc, qc, K, out_dt, sms, stream)
+         : best == 128 ? mm_launch<1, 128>(p, pc, qc, K, out_dt, sms, stream)
+                       : mm_launch<1, 64>(p, pc, qc, K, out_dt, sms, stream);
 }
 
 }  // namespace cskv

@@ -61,6 +61,25 @@ def test_many_tiles_a_cta():
     _check(api.mxfp4_matmul(a[:20].contiguous(), ae[:20].contiguous(), b, be), av[:20], bv)
 
 
+@pytest.mark.parametrize("M,N,K", [(4096, 4096, 544), (4000, 4001, 288)])
+def test_large_tiles(M, N, K):
+    """256-row tiles, several a CTA: sampled rows and columns against float64, every element against
+    fp32 (both sums are off by K 2^-23 sum|a b| at most)."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    a, ae = api.mxfp4_quantize(torch.randn(M, K, device="cuda", generator=g))
+    b, be = api.mxfp4_quantize(torch.randn(N, K, device="cuda", generator=g))
+    av, bv = (api.mxfp4_dequantize(x, y, dtype=torch.float32) for x, y in ((a, ae), (b, be)))
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = api.mxfp4_matmul(a, ae, b, be, dtype=torch.float32, dev_status=st)
+    assert int(st.item()) == 0
+    mag = av.abs() @ bv.abs().T
+    assert bool(((out - av @ bv.T).abs() <= 2 * K * 2.0 ** -23 * 1.01 * mag).all())
+    rows = torch.tensor([0, 127, 128, 255, 256, M // 2, M - 1], device="cuda")
+    _check(out[rows], to_f64(av[rows]), to_f64(bv))
+    out16 = api.mxfp4_matmul(a, ae, b, be)
+    assert torch.equal(out16, out.to(torch.bfloat16))
+
+
 def test_each_element_meets_its_scale():
     """One nonzero element a row, at every place of a block row: a wrong scale, row or K order shows."""
     K = 576
