@@ -24,7 +24,8 @@ constexpr int kMmThreads = 448;          // warp 0 TMA, 1 products, 2-5 scales, 
 constexpr int kMmScaleWarps = 4, kMmOutWarp = 2 + kMmScaleWarps;
 constexpr int kMmDeep = 256;             // codes of a stage: 128 bytes a row
 constexpr uint32_t kMmTileP = 128 * 128;  // bytes of 128 rows' codes
-constexpr int kMmSfStep = 32;            // TMEM columns of one stage's scales
+constexpr uint32_t kMmOutPad = 144;       // bytes of a staged output row: 128 and a skew of four banks
+constexpr uint32_t kMmOutWarp32 = 32 * kMmOutPad;  // an output warp's staging
 constexpr int kMmMaxSplit = 8;           // CTAs of a cluster that share a tile's inner length
 
 struct MmParams {
@@ -47,13 +48,15 @@ struct MmShape {
   static constexpr uint32_t codes = MT * kMmTileP + NQ * 128u;   // a stage's code bytes
   static constexpr uint32_t scales = 1024u * (MT + qc);          // two K chunks each
   static constexpr uint32_t stage = (codes + scales + 1023u) / 1024u * 1024u;
-  static constexpr int stages = (int)(196608u / stage) < 8 ? (int)(196608u / stage) : 8;
-  static constexpr size_t smem = (size_t)stage * stages + 1024;
+  static constexpr int stages = (int)(188416u / stage) < 8 ? (int)(188416u / stage) : 8;
+  static constexpr size_t smem = (size_t)stage * stages + 4 * MT * kMmOutWarp32 + 1024;
   static constexpr int acc_cols = NQ < 32 ? 32 : NQ;             // TMEM columns of 128 rows' accumulator
   static constexpr int accs = MT == 1 ? 2 : 1;                   // tiles in tensor memory
   static constexpr int sf_col = 2 * acc_cols;
-  static constexpr int cols = sf_col + 2 * kMmSfStep <= 128 ? 128 : sf_col + 2 * kMmSfStep <= 256 ? 256 : 512;
-  static_assert(sf_col + 2 * kMmSfStep <= 512 && 8 * (MT + qc) <= kMmSfStep, "tensor memory");
+  static constexpr int sf_step = 8 * (MT + qc);                  // TMEM columns of a stage's scales
+  static constexpr int used = sf_col + stages * sf_step;
+  static constexpr int cols = used <= 128 ? 128 : used <= 256 ? 256 : 512;
+  static_assert(used <= 512, "tensor memory");
   static_assert((size_t)stage * stages >= 128u * NQ * 4u, "a split tile's partial fits the ring");
 };
 
@@ -103,18 +106,6 @@ __device__ __forceinline__ void mm_store(const MmParams& p, int64_t pr, int64_t 
     return;
   }
   T* dst = out + pr * p.ld + q;
-  if constexpr (STEP % 8 == 0) {
-    if (whole && (p.ld * sizeof(T)) % 16 == 0) {  // rows of out, and q's multiples of 8, are 16-byte places
-#pragma unroll
-      for (int i = 0; i < STEP; i += 8) {
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = v[i + j];
-        Vec8<T>::store(dst + i, f);
-      }
-      return;
-    }
-  }
 #pragma unroll
   for (int i = 0; i < STEP; ++i)
     if (whole || q + i < p.q_rows) dst[i] = one(v[i]);
@@ -186,42 +177,58 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- products
-    if (lane == 0) {
-      const uint32_t base = smem_u32(buf);
-      uint32_t g = 0, n = 0;
-      bool ok = true;
-      for (int64_t tile = tile0; tile < tiles && ok; tile += stride, ++n) {
-        const uint32_t ab = n % Sh::accs;
-        if (n >= Sh::accs) ok = role_wait(&sh.acc_empty[ab], n / Sh::accs - 1, &sh.abort, p.st);
-        tc_fence_after();
-        for (int k = k0; k < k1 && ok; ++k, ++g) {
-          const uint32_t s = g % Sh::stages, at = base + s * Sh::stage, sf = at + Sh::codes;
-          ok = role_wait(&sh.full[s], g / Sh::stages, &sh.abort, p.st) &&
-               role_wait(&sh.sf_full[s], g / Sh::stages, &sh.abort, p.st);
-          if (!ok) break;
-          tc_fence_after();
-          // scales, 512 bytes a chunk of 128 rows and 4 K scales: P's subtiles (two K chunks each), then
-          // Q's rows by K chunk
-          const uint32_t col = tmem + Sh::sf_col + (g & 1) * kMmSfStep;
+    // A step's descriptors differ by their address field alone (16-byte units).
+    const uint32_t base = smem_u32(buf);
+    const uint64_t d_codes = smem_desc_sw128(base, 16, 1024), d_scales = smem_desc_noswz(base + Sh::codes, 16, 128);
+    uint32_t n = 0, s = 0, sp = 0, ss = 0, ssp = 0;  // stage and phase of the products, of the scales
+    bool ok = true;
+    // Scales of a step -> tensor memory, 512 bytes a chunk of 128 rows and 4 K scales: P's subtiles
+    // (two K chunks each), then Q's rows by K chunk.  A stage has columns of its own: the products
+    // that read them last are complete when its scales have been replaced.
+    auto copy_scales = [&]() {
+      if (!role_wait_warp(&sh.sf_full[ss], ssp, &sh.abort, p.st)) return false;
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
-          for (int c = 0; c < 2 * (MT + Sh::qc); ++c)
-            tc_cp_scales(col + 4 * c, smem_desc_noswz(sf + 512 * c, 16, 128));
+        for (int i = 0; i < 2 * (MT + Sh::qc); ++i)
+          tc_cp_scales(tmem + Sh::sf_col + ss * Sh::sf_step + 4 * i, d_scales + ss * (Sh::stage >> 4) + 32 * i);
+      }
+      __syncwarp();
+      if (++ss == Sh::stages) ss = 0, ssp ^= 1;
+      return true;
+    };
+    for (int64_t tile = tile0; tile < tiles && ok; tile += stride, ++n) {
+      const uint32_t ab = n % Sh::accs;
+      if (n >= Sh::accs) ok = role_wait_warp(&sh.acc_empty[ab], n / Sh::accs - 1, &sh.abort, p.st);
+      tc_fence_after();
+      for (int k = k0; k < k1 && ok; ++k) {
+        // a step's scales go out before the products of the step before it, which need not wait for
+        // them then
+        if (k == k0) ok = copy_scales();
+        if (ok && k + 1 < k1) ok = copy_scales();
+        ok = ok && role_wait_warp(&sh.full[s], sp, &sh.abort, p.st);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t col = tmem + Sh::sf_col + s * Sh::sf_step;
+        const uint64_t d = d_codes + s * (Sh::stage >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc_mma_mxf4(tmem + (MT == 1 ? ab : mt) * Sh::acc_cols,
-                          smem_desc_sw128(at + mt * kMmTileP + 32 * kk, 16, 1024),
-                          smem_desc_sw128(at + MT * kMmTileP + 32 * kk, 16, 1024), idesc_mxf4(128, NQ, 2 * (kk & 1)),
+              tc_mma_mxf4(tmem + (MT == 1 ? ab : mt) * Sh::acc_cols, d + (mt * kMmTileP + 32 * kk) / 16,
+                          d + (MT * kMmTileP + 32 * kk) / 16, idesc_mxf4(128, NQ, 2 * (kk & 1)),
                           col + 8 * mt + 4 * (kk >> 1), col + 8 * MT + 4 * Sh::qc * (kk >> 1), k > k0 || kk > 0);
           tc_commit(&sh.empty[s]);
+          if (k + 1 == k1) tc_commit(&sh.acc_full[ab]);
         }
-        if (ok) tc_commit(&sh.acc_full[ab]);
+        __syncwarp();
+        if (++s == Sh::stages) s = 0, sp ^= 1;
       }
-      if (!ok) {  // gave up: nothing of this CTA may still be in flight when its memory is released
-        tc_commit(&sh.bail);
-        mbar_wait_bounded(&sh.bail, 0);
-      }
+    }
+    if (!ok && elect_one()) {  // gave up: nothing of this CTA may still be in flight when its memory is released
+      tc_commit(&sh.bail);
+      mbar_wait_bounded(&sh.bail, 0);
     }
     __syncwarp();
   } else if (warp < kMmOutWarp) {
@@ -271,6 +278,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
     const int quad = warp & 3, mt = (warp - kMmOutWarp) >> 2;  // the TMEM lanes this warp may read
     const int row_in = quad * 32 + lane;
     constexpr int kStep = NQ < 32 ? 16 : 32;
+    uint8_t* cross = buf + Sh::stage * Sh::stages + (warp - kMmOutWarp) * kMmOutWarp32;
+    const bool wide_out = p.p_is_a && (p.ld * sizeof(T)) % 16 == 0;  // every 8th column is a 16-byte place
     uint32_t n = 0;
     bool ok = mt < MT;
     for (int64_t tile = tile0; tile < tiles && ok; tile += stride, ++n) {
@@ -292,7 +301,27 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
         float f[kStep];
 #pragma unroll
         for (int i = 0; i < kStep; ++i) f[i] = __uint_as_float(v[i]);
-        if (split == 1) {
+        if (split == 1 && kStep == 32 && wide_out && q0 + c + 32 <= p.q_rows) {
+          // out[p, q]: the warp's 32 x 32 values cross in shared memory, so that lanes store whole
+          // stretches of a row (64 or 128 bytes) instead of 16 bytes of 32 rows
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = f[(i + j) % kStep];
+            Vec8<T>::store(reinterpret_cast<T*>(cross + lane * kMmOutPad) + i, x);
+          }
+          __syncwarp();
+          constexpr int kLanes = 2 * sizeof(T);  // lanes of a row: 16 bytes each
+#pragma unroll
+          for (int i = 0; i < kLanes; ++i) {
+            const int r = i * (32 / kLanes) + lane / kLanes, at = lane % kLanes;
+            const uint4 w = *reinterpret_cast<const uint4*>(cross + r * kMmOutPad + 16 * at);
+            if (pr - lane + r < p.p_rows)
+              *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + (pr - lane + r) * p.ld + q0 + c + at * (16 / sizeof(T))) = w;
+          }
+          __syncwarp();
+        } else if (split == 1) {
           mm_store<kStep, T>(p, pr, q0 + c, f);
         } else {
 #pragma unroll
