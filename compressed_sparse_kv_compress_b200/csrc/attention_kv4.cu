@@ -253,68 +253,74 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
       }
       cp_async_wait_all();
     } else if (warp == k4Mma) {
-      // ---------------------------------------------------------------- MMA issue
-      if (lane == 0) {
-        const uint32_t kv = smem_u32(buf);
-        uint32_t g = 0, n = 0;
-        bool ok = true;
-        auto issue_s = [&](uint32_t c) {
-          const uint32_t st = c % k4KStages;
-          if (!k4_wait(sh, &sh.k_full[st], c / k4KStages, p.st)) return false;
-          tc_fence_after();
-          const int nc = sh.meta[c % k4Table].nc;
+      // -------------------------------------------------------------- MMA issue
+      // Descriptors differ by their address field alone (16-byte units).
+      const uint32_t kv = smem_u32(buf);
+      const uint64_t d_k = smem_desc_sw128(kv, 16, 1024), d_v = smem_desc_sw128(kv + k4OffV, k4Region, 1024);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(128, 128, false, true);
+      uint32_t g = 0, n = 0;
+      bool ok = true;
+      auto issue_s = [&](uint32_t c) {
+        const uint32_t st = c % k4KStages;
+        if (!k4_wait_warp(sh, &sh.k_full[st], c / k4KStages, p.st)) return false;
+        tc_fence_after();
+        const int nc = sh.meta[c % k4Table].nc;
+        const uint32_t idesc = idesc_bf16_f32(128, nc, false, false), tS = tmem + (c & 1) * 128;
+        const uint64_t d = d_k + st * (k4Half >> 4);
+        if (elect_one()) {
           if (nc) {
-            const uint32_t idesc = idesc_bf16_f32(128, nc, false, false);
-#pragma unroll 1
+#pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              tc_mma_f16_ta(tmem + (c & 1) * 128, tmem + k4ColQ + kk * 8,
-                            smem_desc_sw128(kv + st * k4Half + (uint32_t)(kk >> 2) * k4Region + (uint32_t)(kk & 3) * 32,
-                                            16, 1024),
-                            idesc, kk > 0);
+              tc_mma_f16_ta(tS, tmem + k4ColQ + kk * 8, d + (kk >> 2) * (k4Region >> 4) + (kk & 3) * 2, idesc, kk > 0);
           }
           tc_commit(&sh.k_empty[st]);
           tc_commit(&sh.s_full[c & 1]);
           mbar_arrive(&sh.s_full[c & 1]);  // passes the chunk's notes on to the softmax warps
-          return true;
-        };
-        for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x, ++n) {
-          ok = k4_wait(sh, &sh.q_full, n, p.st);
-          tc_fence_after();
-          ok = ok && issue_s(g);
-          bool first = true;
-          for (bool more = true; more && ok; ++g) {
-            const uint32_t st = g % k4VStages;
-            const int nc = sh.meta[g % k4Table].nc;
-            more = !sh.meta[g % k4Table].last;
-            // the next chunk's S goes first if its K is there before this chunk's P
-            bool ahead = false;
-            if (more) {
-              for (int i = 0; i < (1 << 22) && !ahead && !mbar_test(&sh.p_full[g & 1], (g >> 1) & 1u); ++i) {
-                if (mbar_try_wait(&sh.k_full[(g + 1) % k4KStages], ((g + 1) / k4KStages) & 1u)) {
-                  ahead = true;
-                  ok = issue_s(g + 1);
-                }
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x, ++n) {
+        ok = k4_wait_warp(sh, &sh.q_full, n, p.st);
+        tc_fence_after();
+        ok = ok && issue_s(g);
+        bool first = true;
+        for (bool more = true; more && ok; ++g) {
+          const uint32_t st = g % k4VStages;
+          const int nc = sh.meta[g % k4Table].nc;
+          more = !sh.meta[g % k4Table].last;
+          // the next chunk's S goes first if its K is there before this chunk's P
+          bool ahead = false;
+          if (more) {
+            for (int i = 0; i < (1 << 22) && !ahead && !__all_sync(0xffffffffu, mbar_test(&sh.p_full[g & 1], (g >> 1) & 1u)); ++i) {
+              if (__all_sync(0xffffffffu, mbar_try_wait(&sh.k_full[(g + 1) % k4KStages], ((g + 1) / k4KStages) & 1u))) {
+                ahead = true;
+                ok = issue_s(g + 1);
               }
             }
-            ok = ok && k4_wait(sh, &sh.v_full[st], g / k4VStages, p.st) && k4_wait(sh, &sh.p_full[g & 1], g >> 1, p.st);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t idesc = idesc_bf16_f32(128, 128, false, true);
-#pragma unroll 1
-            for (int kk = 0; kk < nc / 16; ++kk)
-              tc_mma_f16_ta(tmem + k4ColO, tmem + (g & 1) * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
-                            smem_desc_sw128(kv + k4OffV + st * k4Half + (uint32_t)kk * 2048, k4Region, 1024), idesc,
-                            !first || kk > 0);
-            if (nc) first = false;
+          }
+          ok = ok && k4_wait_warp(sh, &sh.v_full[st], g / k4VStages, p.st) &&
+               k4_wait_warp(sh, &sh.p_full[g & 1], g >> 1, p.st);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t tP = tmem + (g & 1) * 128;
+          const uint64_t d = d_v + st * (k4Half >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              if (kk * 16 < nc)
+                tc_mma_f16_ta(tmem + k4ColO, tP + (kk >> 2) * 64 + (kk & 3) * 8, d + kk * 128, idesc_o, !first || kk > 0);
             tc_commit(&sh.v_empty[st]);
             tc_commit(&sh.o_done);
-            if (more && !ahead) ok = issue_s(g + 1);
           }
+          __syncwarp();
+          if (nc) first = false;
+          if (more && !ahead) ok = issue_s(g + 1);
         }
-        if (!ok) {  // gave up: nothing of this CTA may still be in flight when its memory is released
-          tc_commit(&sh.bail);
-          mbar_wait_bounded(&sh.bail, 0);
-        }
+      }
+      if (!ok && elect_one()) {  // gave up: nothing of this CTA may still be in flight when its memory is released
+        tc_commit(&sh.bail);
+        mbar_wait_bounded(&sh.bail, 0);
       }
       __syncwarp();
     }
