@@ -19,9 +19,9 @@
 //   warps 8-15  decode them to bf16 in the 128-byte-swizzle layout, 16 rows a warp
 //   warp 18     one thread issues S = Q K^T and O (+)= P V; Q and P are A operands in tensor
 //               memory, so only K and V are read from shared memory
-//   warps 0-7   softmax: TMEM lane h is head h; S -> P, O rescaled when the running maximum grows by
-//               more than 2^8 (any reference serves the online softmax), output
-// Two K and three V buffers (32 KB each) and two S buffers pipeline the chunks, across queries
+//   warps 0-7   softmax: TMEM lane h is head h; S -> P in place, O rescaled when the running
+//               maximum grows by more than 2^8 (any reference serves the online softmax), output
+// Two K and three V buffers (32 KB each) and two S / P buffers pipeline the chunks, across queries
 // too.  The roles' loops are kept short: unrolled ones missed the instruction cache.
 #include "attn_rows.cuh"
 #include "mx4.cuh"
@@ -40,7 +40,7 @@ constexpr uint32_t k4Half = 2 * k4Region;               // a chunk's K (or V): d
 constexpr uint32_t k4OffV = k4KStages * k4Half, k4OffRaw = k4OffV + k4VStages * k4Half;
 constexpr uint32_t k4Raw = k4Chunk * kKv4RowBytes;      // a chunk's rows as stored
 constexpr size_t k4Smem = k4OffRaw + k4RawStages * k4Raw + 1024;
-constexpr uint32_t k4ColO = 256, k4ColQ = 384, k4ColP = 448;  // TMEM: S buffers at 0 and 128, O, Q, P
+constexpr uint32_t k4ColO = 256, k4ColQ = 384;          // TMEM: S/P buffers at 0 and 128, O, Q
 constexpr float k4Grow = 8.f;                           // log2: growth of the maximum that rescales
 
 struct K4Chunk {
@@ -53,14 +53,11 @@ struct K4Chunk {
 struct K4Shared {
   uint64_t tab_full[k4Table], tab_empty[k4Table], k_full[k4KStages], k_empty[k4KStages], v_full[k4VStages];
   uint64_t raw_full[k4RawStages], raw_empty[k4RawStages];
-  uint64_t v_empty[k4VStages], s_full[2], p_full, max_full[4], sum_full[4];
-  uint64_t half_full[4], half_empty[4], o_done, q_full, bail;
+  uint64_t v_empty[k4VStages], s_full[2], p_full[2], max_full[4], sum_full[4], o_done, q_full, bail;
   uint32_t tmem;
   int abort;
   K4Chunk tab_meta[k4Table], meta[k4Table];
-  float half_max[2][2][128], half_sum[2][128];  // [chunk parity][column half][lane], [half][lane]
-  float half_o[4][16][32];                      // sixteen dims of the upper lanes' rows, and their (m, l)
-  float2 half_ml[4][32];
+  float half_max[2][2][128], half_sum[2][128];  // [chunk parity][column half][head], [half][head]
   uint64_t row[k4Table][k4Chunk];               // address of each row; 0: skipped
 };
 
@@ -118,11 +115,7 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
   const int S = p.max_splits, H = p.H;
   const int64_t items = (int64_t)p.T * S;
 
-  // Up to 64 heads: Q fills the tile twice, so S comes out in both halves of the lanes, and the upper
-  // 64 lanes take the upper 64 columns: all four schedulers share the softmax.  P is zero where a
-  // lane does not own the column, and a head's O is the sum of its two lanes' rows.
-  const bool twice = H <= 64;
-  const int quads = (H + 31) / 32, soft = (twice ? 4 : 2) * quads;  // lane groups of the heads, softmax warps at work
+  const int quads = (H + 31) / 32, soft = 2 * quads;  // TMEM lane groups with heads, softmax warps at work
 
   // ---- set-up that reads no input overlaps the previous kernel (dependent launch)
   if (warp == k4Mma) {
@@ -148,14 +141,12 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 2);
+      mbar_init(&sh.p_full[i], soft);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sh.max_full[i], 2);
       mbar_init(&sh.sum_full[i], 2);
-      mbar_init(&sh.half_full[i], 1);
-      mbar_init(&sh.half_empty[i], 1);
     }
-    mbar_init(&sh.p_full, soft);
     mbar_init(&sh.o_done, 1);
     mbar_init(&sh.q_full, soft);
     mbar_init(&sh.bail, 1);
@@ -301,7 +292,7 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
           // the next chunk's S goes first if its K is there before this chunk's P
           bool ahead = false;
           if (more) {
-            for (int i = 0; i < (1 << 22) && !ahead && !__all_sync(0xffffffffu, mbar_test(&sh.p_full, g & 1u)); ++i) {
+            for (int i = 0; i < (1 << 22) && !ahead && !__all_sync(0xffffffffu, mbar_test(&sh.p_full[g & 1], (g >> 1) & 1u)); ++i) {
               if (__all_sync(0xffffffffu, mbar_try_wait(&sh.k_full[(g + 1) % k4KStages], ((g + 1) / k4KStages) & 1u))) {
                 ahead = true;
                 ok = issue_s(g + 1);
@@ -309,15 +300,16 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
             }
           }
           ok = ok && k4_wait_warp(sh, &sh.v_full[st], g / k4VStages, p.st) &&
-               k4_wait_warp(sh, &sh.p_full, g, p.st);
+               k4_wait_warp(sh, &sh.p_full[g & 1], g >> 1, p.st);
           if (!ok) break;
           tc_fence_after();
+          const uint32_t tP = tmem + (g & 1) * 128;
           const uint64_t d = d_v + st * (k4Half >> 4);
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               if (kk * 16 < nc)
-                tc_mma_f16_ta(tmem + k4ColO, tmem + k4ColP + kk * 8, d + kk * 128, idesc_o, !first || kk > 0);
+                tc_mma_f16_ta(tmem + k4ColO, tP + (kk >> 2) * 64 + (kk & 3) * 8, d + kk * 128, idesc_o, !first || kk > 0);
             tc_commit(&sh.v_empty[st]);
             tc_commit(&sh.o_done);
           }
@@ -398,42 +390,33 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
     }
   } else {
     // ---------------------------------------------------------------- softmax and output
-    // Warps w and w + 4 share the TMEM lanes 32w .. 32w + 31: each takes half of the lanes' columns, of
-    // Q's and of O's dims, and they exchange row maxima and sums.
-    const int quad = warp & 3, half = warp >> 2, lane_id = quad * 32 + lane;
-    const int upper = twice ? quad >> 1 : 0;                         // lanes that take columns 64 ..
-    const int h = twice ? (quad & 1) * 32 + lane : lane_id;          // head of this lane
-    const int ncol = twice ? 32 : 64, col0 = 64 * upper + ncol * half;
-    const bool active = (twice ? (quad & 1) : quad) < quads;
+    // warps w and w + 4 share the TMEM lanes of heads 32w .. 32w + 31: each takes half of a
+    // chunk's columns, of Q's and of O's dims, and they exchange row maxima and sums
+    const int quad = warp & 3, half = warp >> 2, h = quad * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     const float sl2 = p.scale_log2;
     const float sk = (p.sink && h < H) ? __ldg(p.sink + h) * kLog2e : -INFINITY;
     auto put_q = [&](int64_t item) {
-      const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
-                                                        ((size_t)(item / S) * H + h) * kHeadDim + 64 * half);
-      uint32_t v[32];
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
+                                                          ((size_t)(item / S) * H + h) * kHeadDim + 64 * half);
+        uint32_t v[32];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 w = h < H ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-        v[4 * i] = w.x, v[4 * i + 1] = w.y, v[4 * i + 2] = w.z, v[4 * i + 3] = w.w;
+        for (int i = 0; i < 8; ++i) {
+          const uint4 w = h < H ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+          v[4 * i] = w.x, v[4 * i + 1] = w.y, v[4 * i + 2] = w.z, v[4 * i + 3] = w.w;
+        }
+        tmem_st32(tmem + k4ColQ + lane_base + 32 * half, v);
+        tmem_st_wait();
       }
-      tmem_st32(tmem + k4ColQ + lane_base + 32 * half, v);
-      tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full);
     };
-    uint32_t g = 0, n = 0, rounds = 0;  // chunks, items, exchanges of O done
+    uint32_t g = 0, n = 0;
     bool ok = true;
-    if (active && twice) {  // P of the columns that the other half of the lanes owns stays zero
-      uint32_t z[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) z[i] = 0u;
-      tmem_st16(tmem + k4ColP + lane_base + 32 * (upper ^ 1) + 16 * half, z);
-      tmem_st_wait();
-    }
-    if (active && blockIdx.x < items) put_q(blockIdx.x);
-    for (int64_t item = active ? blockIdx.x : items; item < items && ok; item += gridDim.x, ++n) {
+    if (quad < quads && blockIdx.x < items) put_q(blockIdx.x);
+    for (int64_t item = quad < quads ? blockIdx.x : items; item < items && ok; item += gridDim.x, ++n) {
       float m = -INFINITY, l = 0.f;
       bool filled = false;  // O holds something
       for (bool more = true; more; ++g) {
@@ -443,12 +426,11 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
         tc_fence_after();
         const int nc = sh.meta[st].nc;
         more = !sh.meta[st].last;
-        const uint32_t tS = tmem + sp * 128 + col0 + lane_base;
+        const uint32_t tS = tmem + sp * 128 + 64 * half + lane_base;
         if (nc) {
-          // this warp's columns, 16 at a time; those past nc hold old values, and their mask bits are
-          // clear
-          const uint32_t* mask = sh.meta[st].mask + (col0 >> 5);
-          const uint64_t vm = (uint64_t)(twice ? 0u : mask[1]) << 32 | mask[0];
+          // this half's 64 columns, 16 at a time; those past nc hold old values, and their mask bits
+          // are clear
+          const uint64_t vm = (uint64_t)sh.meta[st].mask[2 * half + 1] << 32 | sh.meta[st].mask[2 * half];
           auto columns = [&](int c, uint32_t (&v)[16]) {
             tmem_ld16(tS + c, v);
             tmem_ld_wait();
@@ -461,7 +443,7 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
           };
           float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-          for (int c = 0; c < ncol; c += 16) {
+          for (int c = 0; c < 64; c += 16) {
             uint32_t v[16];
             columns(c, v);
 #pragma unroll
@@ -469,23 +451,19 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
               mx4[(i >> 1) & 3] = fmaxf(mx4[(i >> 1) & 3], fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
           }
           float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          sh.half_max[sp][half][lane_id] = mx;
+          sh.half_max[sp][half][h] = mx;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.max_full[quad]);
           ok = k4_wait_warp(sh, &sh.max_full[quad], g, p.st);
           if (!ok) break;
-          mx = fmaxf(mx, sh.half_max[sp][half ^ 1][lane_id]) * sl2;
+          mx = fmaxf(mx, sh.half_max[sp][half ^ 1][h]) * sl2;
           const float m_new = mx > m + k4Grow || m == -INFINITY ? fmaxf(mx, m) : m;
           const float alpha = m_new == -INFINITY || m_new == m ? 1.f : fast_exp2(m - m_new);
           const float nm = m_new == -INFINITY ? 0.f : -m_new;
-          // the last chunk's product has read P, and O is complete
-          if (g > 0) ok = k4_wait_warp(sh, &sh.o_done, g - 1, p.st);
-          if (!ok) break;
-          tc_fence_after();
-          // P = 2^(s scale - m) as bf16
+          // P = 2^(s scale - m) as bf16, over this half's columns that have been read
           float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-          for (int c = 0; c < ncol; c += 16) {
+          for (int c = 0; c < 64; c += 16) {
             uint32_t v[16], w[8];
             columns(c, v);
 #pragma unroll
@@ -496,10 +474,14 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
               const __nv_bfloat162 e = __floats2bfloat162_rn(e0, e1);
               w[i] = *reinterpret_cast<const uint32_t*>(&e);
             }
-            tmem_st8(tmem + k4ColP + lane_base + ((col0 + c) >> 1), w);
+            tmem_st8(tS + (c >> 1), w);
           }
-          // tensor-memory accesses are warp-wide, so a warp rescales when one of its rows needs it
+          // O of the earlier chunks is rescaled once its last product is complete (tensor-memory
+          // accesses are warp-wide, so a warp rescales when one of its rows needs it)
           if (filled && __any_sync(0xffffffffu, alpha != 1.f)) {
+            ok = k4_wait_warp(sh, &sh.o_done, g - 1, p.st);
+            if (!ok) break;
+            tc_fence_after();
             const uint32_t tO = tmem + k4ColO + lane_base + 64 * half;
 #pragma unroll 1
             for (int cc = 0; cc < 64; cc += 16) {
@@ -520,57 +502,20 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
         filled = filled || nc > 0;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full);
+        if (lane == 0) mbar_arrive(&sh.p_full[sp]);
       }
       if (!ok) break;
       // every S of this query is complete: the next query's Q may take its place
       if (item + gridDim.x < items) put_q(item + gridDim.x);
-      sh.half_sum[half][lane_id] = l;
+      sh.half_sum[half][h] = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.sum_full[quad]);
       ok = k4_wait_warp(sh, &sh.sum_full[quad], n, p.st) && k4_wait_warp(sh, &sh.o_done, g - 1, p.st);
       if (!ok) break;
       tc_fence_after();
-      l += sh.half_sum[half ^ 1][lane_id];
+      l += sh.half_sum[half ^ 1][h];
       const int t = (int)(item / S), split = (int)(item % S);
       const uint32_t tO = tmem + k4ColO + lane_base + 64 * half;
-      const int pair = (quad & 1) * 2 + half;  // a lower and an upper warp with the same heads and dims
-      if (upper) {
-        // the upper lanes' rows go to the lower lanes' warp, sixteen dims at a time
-        if (rounds) ok = k4_wait_warp(sh, &sh.half_empty[pair], rounds - 1, p.st);
-        if (!ok) break;
-        sh.half_ml[pair][lane] = make_float2(m, l);
-#pragma unroll 1
-        for (int cc = 0; cc < 64; cc += 16, ++rounds) {
-          uint32_t v[16];
-          if (cc) ok = k4_wait_warp(sh, &sh.half_empty[pair], rounds - 1, p.st);
-          if (!ok) break;
-          if (filled) {
-            tmem_ld16(tO + cc, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sh.half_o[pair][i][lane] = __uint_as_float(v[i]);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.half_full[pair]);
-        }
-        tc_fence_before();
-        continue;
-      }
-      float fa = 1.f, fb = 0.f;  // factors of the lower and the upper lane's row
-      if (twice) {
-        ok = k4_wait_warp(sh, &sh.half_full[pair], rounds, p.st);
-        if (!ok) break;
-        const float2 b = sh.half_ml[pair][lane];
-        const float M = fmaxf(m, b.x);
-        fa = m == -INFINITY ? 0.f : exp2f(m - M);
-        fb = b.x == -INFINITY ? 0.f : exp2f(b.x - M);
-        l = l * fa + b.y * fb;
-        m = M;
-      }
-      // one split: the output; else a partial for the merge kernel, [query][split][head][dim] and (m, l)
-      // [query][split][head] (m = -inf: no rows, and no partial)
-      const size_t sb = ((size_t)t * S + split) * H + h, row = ((size_t)t * H + h) * kHeadDim + 64 * half;
       if (S == 1) {
         const float M = fmaxf(m, sk);
         float f = 0.f, L = 0.f;
@@ -579,58 +524,51 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
           L = l * f + (p.sink ? exp2f(sk - M) : 0.f);
         }
         const float inv = L > 0.f || L != L ? f / L : 0.f;
-        fa *= inv, fb *= inv;
-        if (half == 0 && h < H && p.lse)
-          p.lse[(size_t)t * H + h] = L > 0.f || L != L ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
-      } else if (half == 0 && h < H) {
-        reinterpret_cast<float2*>(p.part_ml)[sb] = make_float2(m, l);
-      }
+        const size_t row = ((size_t)t * H + h) * kHeadDim + 64 * half;
 #pragma unroll 1
-      for (int cc = 0; cc < 64; cc += 16) {
-        float o[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = 0.f;
-        __syncwarp();
-        if (filled) {
+        for (int cc = 0; cc < 64; cc += 16) {
           uint32_t v[16];
-          tmem_ld16(tO + cc, v);
-          tmem_ld_wait();
-          // a row without attended columns has no O of its own (its factor is 0)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = fa != 0.f ? __uint_as_float(v[i]) * fa : 0.f;
-        }
-        if (twice) {
-          if (cc) ok = k4_wait_warp(sh, &sh.half_full[pair], rounds, p.st);
-          if (!ok) break;
-          if (filled) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] += fb != 0.f ? sh.half_o[pair][i][lane] * fb : 0.f;
-          }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.half_empty[pair]);
-          ++rounds;
-        }
-        if (h < H) {
-          if (S > 1) {
-            if (filled) {
-#pragma unroll
-              for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4*>(p.part_acc + sb * kHeadDim + 64 * half + cc + i) =
-                    make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-            }
-          } else {
+          if (filled) {
+            tmem_ld16(tO + cc, v);
+            tmem_ld_wait();
+          }
+          if (h < H) {
+            // a row without attended columns has no O of its own
 #pragma unroll
             for (int i = 0; i < 16; i += 8) {
-              float x[8];
+              float o[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) x[j] = o[i + j];
+              for (int j = 0; j < 8; ++j) o[j] = filled && inv != 0.f ? __uint_as_float(v[i + j]) * inv : 0.f;
               if (p.out_bf16)
-                Vec8<__nv_bfloat16>::store(reinterpret_cast<__nv_bfloat16*>(p.out) + row + cc + i, x);
+                Vec8<__nv_bfloat16>::store(reinterpret_cast<__nv_bfloat16*>(p.out) + row + cc + i, o);
               else
-                Vec8<float>::store(p.out + row + cc + i, x);
+                Vec8<float>::store(p.out + row + cc + i, o);
             }
           }
         }
+        if (half == 0 && h < H && p.lse)
+          p.lse[(size_t)t * H + h] = L > 0.f || L != L ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+      } else {
+        // partial for the merge kernel: [query][split][head][dim], (m, l) [query][split][head] (m =
+        // -inf: no rows, and no partial)
+        const size_t sb = ((size_t)t * S + split) * H + h;
+        float* dst = p.part_acc + sb * kHeadDim + 64 * half;
+        if (filled) {
+#pragma unroll 1
+          for (int cc = 0; cc < 64; cc += 16) {
+            uint32_t v[16];
+            __syncwarp();
+            tmem_ld16(tO + cc, v);
+            tmem_ld_wait();
+            if (h < H) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<uint4*>(dst + cc + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+          }
+        }
+        if (half == 0 && h < H) reinterpret_cast<float2*>(p.part_ml)[sb] = make_float2(m, l);
       }
       tc_fence_before();
     }
