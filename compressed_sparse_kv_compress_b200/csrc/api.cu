@@ -481,6 +481,13 @@ size_t hybrid_attn_workspace_size(int mode, int T, int H, int d, int k, int wind
     const size_t need = (size_t)T * pl.ws_splits * H * (kHeadDim + 2) * sizeof(float);
     if (need > best) best = need;
   }
+  {  // the 4-bit rows' plan: at most an SM's worth of heads each, so under the allocation-free scratch
+    int sms = 0, R = 0, S = 0;
+    if (device_sms(&sms)) return 0;
+    attn_kv4_plan(T, (mode == CSKV_CSA ? (int64_t)k : max_entries) + window, sms, &R, &S);
+    const size_t need = S > 1 ? (size_t)T * S * H * (kHeadDim + 2) * sizeof(float) : 0;
+    if (need > best) best = need;
+  }
   if (mode == CSKV_HCA && H == kPairHeads && T >= 2) {  // the pair plan: (T + 1) / 2 units of 2H heads
     AttnPlan pl;
     const int Tp = (T + 1) / 2;
@@ -540,11 +547,11 @@ int hybrid_decode_attn(int mode, const void* q, const void* kv_cmp, const int64_
   if (rc) return rc;
   int sms = 0;
   if (tc && kv4) {
-    // the 4-bit kernel's own plan, inside the workspace that the call without the flag would need
+    // the 4-bit kernel's own plan
     rc = device_sms(&sms);
     if (rc) return rc;
     pl.cluster = 0;
-    attn_kv4_plan(T, (mode == CSKV_CSA ? (int64_t)k : max_entries) + window, pl.ws_splits, sms, &pl.R, &pl.S);
+    attn_kv4_plan(T, (mode == CSKV_CSA ? (int64_t)k : max_entries) + window, sms, &pl.R, &pl.S);
     pl.ws_splits = pl.S;
   }
   // adjacent-query pairs: the HCA tensor-core kernel with 64 heads, when the pairs' plan merges

@@ -583,16 +583,16 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
 }
 
 // Merges the splits of a query ([TR] §3.1), the sink once ([SW] §十二): M = max(max_s m_s, sink),
-// L = sum_s 2^(m_s - M) l_s + 2^(sink - M), o = sum_s 2^(m_s - M) acc_s / L.  A CTA a head, its four
-// warps a quarter of the splits each, a lane four dims.  Bound by latency: eight splits' loads go
-// out together.
-constexpr int k4MergeWarps = 4;
+// L = sum_s 2^(m_s - M) l_s + 2^(sink - M), o = sum_s 2^(m_s - M) acc_s / L.  A CTA a head, its two to
+// eight warps a share of the splits each, a lane four dims.  Bound by latency: eight splits' loads
+// of a warp go out together.
+constexpr int k4MergeWarps = 8;
 
 __global__ void __launch_bounds__(32 * k4MergeWarps) attn_kv4_merge_kernel(const __grid_constant__ AttnParams p) {
   __shared__ float4 part[k4MergeWarps][32];
   __shared__ float part_l[k4MergeWarps];
   const int t = blockIdx.y, h = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int H = p.H, S = p.max_splits;
+  const int H = p.H, S = p.max_splits, warps = blockDim.x >> 5;
   pdl_launch_dependents();
   pdl_wait();
   const size_t sb = (size_t)t * S * H + h;
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(32 * k4MergeWarps) attn_kv4_merge_kernel(const
   float L = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int s = warp; s < S; s += k4MergeWarps) {
+  for (int s = warp; s < S; s += warps) {
     const float2 x = __ldcg(ml + (size_t)s * H);
     const float4 a = __ldcg(acc + (size_t)s * H * (kHeadDim / 4));
     if (x.x != -INFINITY) {
@@ -618,8 +618,7 @@ __global__ void __launch_bounds__(32 * k4MergeWarps) attn_kv4_merge_kernel(const
   if (lane == 0) part_l[warp] = L;
   __syncthreads();
   if (warp) return;
-#pragma unroll
-  for (int w = 1; w < k4MergeWarps; ++w) {
+  for (int w = 1; w < warps; ++w) {
     const float4 a = part[w][lane];
     o.x += a.x, o.y += a.y, o.z += a.z, o.w += a.w;
     L += part_l[w];
@@ -637,18 +636,16 @@ __global__ void __launch_bounds__(32 * k4MergeWarps) attn_kv4_merge_kernel(const
   if (lane == 0 && p.lse) p.lse[(size_t)t * H + h] = L > 0.f || L != L ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
 }
 
-// Splits of a query: whole chunks, as many as fill the SMs once; `most` bounds them by the
-// workspace.
-void attn_kv4_plan(int T, int64_t rows_max, int most, int sms, int* R, int* S) {
-  const int64_t chunks = (rows_max + k4Chunk - 1) / k4Chunk;
-  int64_t s = T < sms ? sms / T : 1;
-  s = s < most ? s : most;
-  s = s < chunks ? s : chunks;
-  if (s < 1) s = 1;
-  const int64_t per = (chunks + s - 1) / s;
+// Splits of a query: whole chunks, as many as fill the SMs once, but no more than pay: a chunk takes
+// about 1.5 us, a split more about 0.05 us of the merge.
+void attn_kv4_plan(int T, int64_t rows_max, int sms, int* R, int* S) {
+  const int64_t chunks = rows_max > 0 ? (rows_max + k4Chunk - 1) / k4Chunk : 1;
+  const int64_t can = T < sms ? sms / T : 1, one = (chunks + can - 1) / can;
+  int64_t per = one;  // chunks of a split
+  auto cost = [&](int64_t n) { return 30 * n + (chunks + n - 1) / n; };
+  while (per < 2 * one && per < chunks && cost(per + 1) < cost(per)) ++per;
   *R = (int)(per * k4Chunk);
-  *S = (int)(chunks ? (chunks + per - 1) / per : 1);
-  if (*R < k4Chunk) *R = k4Chunk;
+  *S = (int)((chunks + per - 1) / per);
 }
 
 cudaError_t launch_attn_kv4(const AttnParams& p, int sms, cudaStream_t stream) {
@@ -660,7 +657,8 @@ cudaError_t launch_attn_kv4(const AttnParams& p, int sms, cudaStream_t stream) {
   if (e != cudaSuccess || p.max_splits == 1) return e;
   e = ensure_smem(attn_kv4_merge_kernel, 0);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(attn_kv4_merge_kernel, dim3(p.H, p.T), dim3(32 * k4MergeWarps), 0, stream, p);
+  const int warps = p.max_splits <= 2 ? 2 : p.max_splits <= 16 ? 4 : k4MergeWarps;
+  e = launch_dependent(attn_kv4_merge_kernel, dim3(p.H, p.T), dim3(32 * warps), 0, stream, p);
   note_launch();
   return e;
 }

@@ -158,7 +158,7 @@ cudaError_t launch_attn_combine(const AttnParams& p, cudaStream_t stream);
 int attn_rows_per_split(int mode, int T, int k, int window, int64_t max_entries, int sms);
 int attn_max_splits(int mode, int k, int window, int64_t max_entries, int R);
 // attention_kv4.cu
-void attn_kv4_plan(int T, int64_t rows_max, int most, int sms, int* R, int* S);
+void attn_kv4_plan(int T, int64_t rows_max, int sms, int* R, int* S);
 cudaError_t launch_attn_kv4(const AttnParams& p, int sms, cudaStream_t stream);
 // api.cu: host-side argument checks of hybrid_decode_attn (all but the workspace)
 int check_attn_args(int mode, const void* q, const void* kv_cmp, const int64_t* cmp_off, const int32_t* idx, int k,
