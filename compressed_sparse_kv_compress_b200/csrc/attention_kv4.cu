@@ -430,12 +430,13 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
         if (nc) {
           // this half's 64 columns, 16 at a time; those past nc hold old values, and their mask bits
           // are clear
-          const uint64_t vm = (uint64_t)sh.meta[st].mask[2 * half + 1] << 32 | sh.meta[st].mask[2 * half];
+          const uint32_t vm0 = sh.meta[st].mask[2 * half], vm1 = sh.meta[st].mask[2 * half + 1];
+          const bool whole = (vm0 & vm1) == 0xFFFFFFFFu;
           auto columns = [&](int c, uint32_t (&v)[16]) {
             tmem_ld16(tS + c, v);
             tmem_ld_wait();
-            const uint32_t b = (uint32_t)(vm >> c) & 0xFFFFu;
-            if (b != 0xFFFFu) {
+            if (!whole) {
+              const uint32_t b = (c < 32 ? vm0 : vm1) >> (c & 31);
 #pragma unroll
               for (int i = 0; i < 16; ++i)
                 if (!((b >> i) & 1u)) v[i] = 0xFF800000u;  // -inf
@@ -461,16 +462,18 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
           const float alpha = m_new == -INFINITY || m_new == m ? 1.f : fast_exp2(m - m_new);
           const float nm = m_new == -INFINITY ? 0.f : -m_new;
           // P = 2^(s scale - m) as bf16, over this half's columns that have been read
-          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t sl2x2 = pack2(sl2, sl2), nmx2 = pack2(nm, nm);
+          uint64_t l2[2] = {0ull, 0ull};
 #pragma unroll 1
           for (int c = 0; c < 64; c += 16) {
             uint32_t v[16], w[8];
             columns(c, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float e0 = fast_exp2(fmaf(__uint_as_float(v[2 * i]), sl2, nm));
-              const float e1 = fast_exp2(fmaf(__uint_as_float(v[2 * i + 1]), sl2, nm));
-              l4[i & 3] += e0 + e1;
+              float e0, e1;
+              unpack2(fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), sl2x2, nmx2), e0, e1);
+              e0 = fast_exp2(e0), e1 = fast_exp2(e1);
+              l2[i & 1] = add2(l2[i & 1], pack2(e0, e1));
               const __nv_bfloat162 e = __floats2bfloat162_rn(e0, e1);
               w[i] = *reinterpret_cast<const uint32_t*>(&e);
             }
@@ -494,7 +497,9 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
             }
           }
           tmem_st_wait();
-          l = l * alpha + ((l4[0] + l4[1]) + (l4[2] + l4[3]));
+          float la, lb;
+          unpack2(add2(l2[0], l2[1]), la, lb);
+          l = l * alpha + (la + lb);
           m = m_new;
         } else if (lane == 0) {
           mbar_arrive(&sh.max_full[quad]);
