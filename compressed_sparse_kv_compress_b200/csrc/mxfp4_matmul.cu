@@ -4,15 +4,15 @@
 // [SW] shareware.cn/news/167317 §六.1 (FP4 suffices for ranking): rows of E2M1 codes with one E8M0
 // scale per 32 values (mx4.cuh), exact products, fp32 accumulation.
 //
-// Large products are bound by what L2 delivers to the SMs (128 x 192 tiles: 41 KB a step, 7.8 TB/s
-// measured; the tensor pipe would take a quarter of that time), so they take 256 x 192 tiles, two
-// products a loaded tile of the other operand; a few rows are bound by the bytes of b and the
-// latency of a step, so few tiles are split over the inner length inside a thread-block cluster.
-// A persistent CTA an SM, with roles: one thread loads code tiles by TMA (128-byte swizzle, 256
-// codes deep, zeros past the edges), four warps load the rows' scales and lay them out as the
-// tensor core wants them, one thread copies scales to tensor memory and issues the products, four
-// or eight warps write out the tile (of 128 rows: while the next one's products run).  The 128-row
-// operand P is a, or, for a few rows of a, b: the tile is then as narrow as those rows.
+// Large products are bound by the tensor pipe (a 128 x 192 tile's step is four products of about 200
+// cycles; its 41 KB arrive in less), a few rows by the latency of a step, so few tiles are split
+// over the inner length inside a thread-block cluster.  A persistent CTA an SM, with roles: one
+// thread loads code tiles by TMA (128-byte swizzle, 256 codes deep, zeros past the edges), four
+// warps load the rows' scales and lay them out as the tensor core wants them, one warp copies
+// scales to tensor memory and issues the products, four warps write out a tile while the next
+// one's products run (two accumulators).  Codes and scales have rings of their own: in one ring a
+// step waited for the slower of the two (4096^3: 50 us).  The 128-row operand P is a, or, for a few
+// rows of a, b: the tile is then as narrow as those rows.
 #include <cuda.h>
 
 #include "launch.cuh"
@@ -20,12 +20,12 @@
 
 namespace cskv {
 
-constexpr int kMmThreads = 448;          // warp 0 TMA, 1 products, 2-5 scales, 6-13 output
+constexpr int kMmThreads = 320;          // warp 0 TMA, 1 products, 2-5 scales, 6-9 output
 constexpr int kMmScaleWarps = 4, kMmOutWarp = 2 + kMmScaleWarps;
 constexpr int kMmDeep = 256;             // codes of a stage: 128 bytes a row
-constexpr uint32_t kMmTileP = 128 * 128;  // bytes of 128 rows' codes
-constexpr uint32_t kMmOutPad = 144;       // bytes of a staged output row: 128 and a skew of four banks
-constexpr uint32_t kMmOutWarp32 = 32 * kMmOutPad;  // an output warp's staging
+constexpr uint32_t kMmTileP = 128 * 128;  // bytes of P's 128 rows of codes
+constexpr int kMmScaleStages = 8;        // a multiple of the scale warps: each meets its own stages in order
+constexpr uint32_t kMmOutPad = 144;      // bytes of a staged output row: 128 and a skew of four banks
 constexpr int kMmMaxSplit = 8;           // CTAs of a cluster that share a tile's inner length
 
 struct MmParams {
@@ -41,27 +41,27 @@ struct MmParams {
   int* st;
 };
 
-// MT x 128 rows of P by NQ of Q.
-template <int MT, int NQ>
+// Tiles of 128 rows of P by NQ of Q.
+template <int NQ>
 struct MmShape {
-  static constexpr int qc = (NQ + 127) / 128;                    // 128-row scale chunks of Q
-  static constexpr uint32_t codes = MT * kMmTileP + NQ * 128u;   // a stage's code bytes
-  static constexpr uint32_t scales = 1024u * (MT + qc);          // two K chunks each
-  static constexpr uint32_t stage = (codes + scales + 1023u) / 1024u * 1024u;
-  static constexpr int stages = (int)(188416u / stage) < 8 ? (int)(188416u / stage) : 8;
-  static constexpr size_t smem = (size_t)stage * stages + 4 * MT * kMmOutWarp32 + 1024;
-  static constexpr int acc_cols = NQ < 32 ? 32 : NQ;             // TMEM columns of 128 rows' accumulator
-  static constexpr int accs = MT == 1 ? 2 : 1;                   // tiles in tensor memory
-  static constexpr int sf_col = 2 * acc_cols;
-  static constexpr int sf_step = 8 * (MT + qc);                  // TMEM columns of a stage's scales
-  static constexpr int used = sf_col + stages * sf_step;
+  static constexpr int qc = (NQ + 127) / 128;                // 128-row scale chunks of Q
+  static constexpr uint32_t codes = kMmTileP + NQ * 128u;    // a stage's code bytes
+  static constexpr uint32_t scales = 1024u * (1 + qc);       // a step's scales: two K chunks each
+  static constexpr int stages = (int)(163840u / codes) < 8 ? (int)(163840u / codes) : 8;
+  static constexpr uint32_t off_scales = codes * stages, off_out = off_scales + scales * kMmScaleStages;
+  static constexpr size_t smem = off_out + 4 * 32 * kMmOutPad + 1024;
+  static constexpr int acc_cols = NQ < 32 ? 32 : NQ;         // TMEM columns of an accumulator
+  // a step's scales in TMEM: when those of step g + 1 are copied, step g's codes are there, so the
+  // products of step g - stages, the last ones that read the same columns, are complete
+  static constexpr int sf_col = 2 * acc_cols, sf_step = 8 * (1 + qc), sf_bufs = stages + 1;
+  static constexpr int used = sf_col + sf_bufs * sf_step;
   static constexpr int cols = used <= 128 ? 128 : used <= 256 ? 256 : 512;
   static_assert(used <= 512, "tensor memory");
-  static_assert((size_t)stage * stages >= 128u * NQ * 4u, "a split tile's partial fits the ring");
+  static_assert(off_scales >= 128u * NQ * 4u, "a split tile's partial fits the ring");
 };
 
 struct MmShared {
-  uint64_t full[8], sf_full[8], empty[8], acc_full[2], acc_empty[2], bail;
+  uint64_t full[8], empty[8], sf_full[kMmScaleStages], sf_empty[kMmScaleStages], acc_full[2], acc_empty[2], bail;
   uint32_t tmem;
   int abort;
 };
@@ -111,9 +111,9 @@ __device__ __forceinline__ void mm_store(const MmParams& p, int64_t pr, int64_t 
     if (whole || q + i < p.q_rows) dst[i] = one(v[i]);
 }
 
-template <int MT, int NQ, typename T>
+template <int NQ, typename T>
 __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __grid_constant__ MmParams p) {
-  using Sh = MmShape<MT, NQ>;
+  using Sh = MmShape<NQ>;
   extern __shared__ __align__(1024) uint8_t smraw[];
   uint8_t* buf = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~(uintptr_t)1023);
   __shared__ MmShared sh;
@@ -135,12 +135,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
   if (tid == 0) {
     for (int i = 0; i < Sh::stages; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.sf_full[i], 1);
       mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < kMmScaleStages; ++i) {
+      mbar_init(&sh.sf_full[i], 1);
+      mbar_init(&sh.sf_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.acc_full[i], 1);
-      mbar_init(&sh.acc_empty[i], 4 * MT);
+      mbar_init(&sh.acc_empty[i], 4);
     }
     mbar_init(&sh.bail, 1);
     sh.abort = 0;
@@ -164,10 +167,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
           const uint32_t s = g % Sh::stages;
           if (g >= Sh::stages) ok = role_wait(&sh.empty[s], g / Sh::stages - 1, &sh.abort, p.st);
           if (!ok) break;
-          uint8_t* dst = buf + s * Sh::stage;
+          uint8_t* dst = buf + s * Sh::codes;
           mbar_arrive_expect_tx(&sh.full[s], Sh::codes);
-          tma_load_2d(dst, &p.p_map, k * 128, pt * (MT * 128), &sh.full[s]);
-          tma_load_2d(dst + MT * kMmTileP, &p.q_map, k * 128, qt * NQ, &sh.full[s]);
+          tma_load_2d(dst, &p.p_map, k * 128, pt * 128, &sh.full[s]);
+          tma_load_2d(dst + kMmTileP, &p.q_map, k * 128, qt * NQ, &sh.full[s]);
         }
       }
       // the last loads have landed before this CTA's memory is released
@@ -179,51 +182,53 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
     // ---------------------------------------------------------------- products
     // A step's descriptors differ by their address field alone (16-byte units).
     const uint32_t base = smem_u32(buf);
-    const uint64_t d_codes = smem_desc_sw128(base, 16, 1024), d_scales = smem_desc_noswz(base + Sh::codes, 16, 128);
-    uint32_t n = 0, s = 0, sp = 0, ss = 0, ssp = 0;  // stage and phase of the products, of the scales
+    const uint64_t d_codes = smem_desc_sw128(base, 16, 1024), d_scales = smem_desc_noswz(base + Sh::off_scales, 16, 128);
+    uint32_t n = 0, s = 0, sp = 0;              // tiles; stage and phase of the codes
+    uint32_t ss = 0, ssp = 0, sb = 0, pb = 0;   // stage and phase of the scales; TMEM buffer of the copies, of the products
+    uint32_t st = 0;                            // scale stage of the products
     bool ok = true;
-    // Scales of a step -> tensor memory, 512 bytes a chunk of 128 rows and 4 K scales: P's subtiles
-    // (two K chunks each), then Q's rows by K chunk.  A stage has columns of its own: the products
-    // that read them last are complete when its scales have been replaced.
+    // Scales of a step -> tensor memory, 512 bytes a chunk of 128 rows and 4 K scales: P's two K chunks,
+    // then Q's rows by K chunk.
     auto copy_scales = [&]() {
       if (!role_wait_warp(&sh.sf_full[ss], ssp, &sh.abort, p.st)) return false;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
-        for (int i = 0; i < 2 * (MT + Sh::qc); ++i)
-          tc_cp_scales(tmem + Sh::sf_col + ss * Sh::sf_step + 4 * i, d_scales + ss * (Sh::stage >> 4) + 32 * i);
+        for (int i = 0; i < 2 * (1 + Sh::qc); ++i)
+          tc_cp_scales(tmem + Sh::sf_col + sb * Sh::sf_step + 4 * i, d_scales + ss * (Sh::scales >> 4) + 32 * i);
       }
       __syncwarp();
-      if (++ss == Sh::stages) ss = 0, ssp ^= 1;
+      if (++ss == kMmScaleStages) ss = 0, ssp ^= 1;
+      if (++sb == Sh::sf_bufs) sb = 0;
       return true;
     };
     for (int64_t tile = tile0; tile < tiles && ok; tile += stride, ++n) {
-      const uint32_t ab = n % Sh::accs;
-      if (n >= Sh::accs) ok = role_wait_warp(&sh.acc_empty[ab], n / Sh::accs - 1, &sh.abort, p.st);
-      tc_fence_after();
+      const uint32_t ab = n & 1;
+      if (n >= 2) ok = role_wait_warp(&sh.acc_empty[ab], n / 2 - 1, &sh.abort, p.st);
       for (int k = k0; k < k1 && ok; ++k) {
+        ok = role_wait_warp(&sh.full[s], sp, &sh.abort, p.st);
         // a step's scales go out before the products of the step before it, which need not wait for
         // them then
-        if (k == k0) ok = copy_scales();
+        if (ok && k == k0) ok = copy_scales();
         if (ok && k + 1 < k1) ok = copy_scales();
-        ok = ok && role_wait_warp(&sh.full[s], sp, &sh.abort, p.st);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t col = tmem + Sh::sf_col + s * Sh::sf_step;
-        const uint64_t d = d_codes + s * (Sh::stage >> 4);
+        const uint32_t col = tmem + Sh::sf_col + pb * Sh::sf_step;
+        const uint64_t d = d_codes + s * (Sh::codes >> 4);
         if (elect_one()) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_mma_mxf4(tmem + (MT == 1 ? ab : mt) * Sh::acc_cols, d + (mt * kMmTileP + 32 * kk) / 16,
-                          d + (MT * kMmTileP + 32 * kk) / 16, idesc_mxf4(128, NQ, 2 * (kk & 1)),
-                          col + 8 * mt + 4 * (kk >> 1), col + 8 * MT + 4 * Sh::qc * (kk >> 1), k > k0 || kk > 0);
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_mxf4(tmem + ab * Sh::acc_cols, d + 2 * kk, d + (kMmTileP >> 4) + 2 * kk,
+                        idesc_mxf4(128, NQ, 2 * (kk & 1)), col + 4 * (kk >> 1), col + 8 + 4 * Sh::qc * (kk >> 1),
+                        k > k0 || kk > 0);
           tc_commit(&sh.empty[s]);
+          tc_commit(&sh.sf_empty[st]);
           if (k + 1 == k1) tc_commit(&sh.acc_full[ab]);
         }
         __syncwarp();
         if (++s == Sh::stages) s = 0, sp ^= 1;
+        if (++st == kMmScaleStages) st = 0;
+        if (++pb == Sh::sf_bufs) pb = 0;
       }
     }
     if (!ok && elect_one()) {  // gave up: nothing of this CTA may still be in flight when its memory is released
@@ -233,37 +238,35 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
     __syncwarp();
   } else if (warp < kMmOutWarp) {
     // ---------------------------------------------------------------- scales
-    // Warp w takes every fourth step (with three stages every third, by three warps: a warp must not
-    // run past a release of a stage that it has not seen).  A row's eight bytes are two words, one for each 512-byte
+    // Warp w takes every fourth step.  A row's eight bytes are two words, one for each 512-byte
     // chunk of 128 rows x 4 K scales: row r at 16 (r % 32) + 4 (r / 32).
-    constexpr int kWarps = Sh::stages < kMmScaleWarps ? Sh::stages : kMmScaleWarps;
-    constexpr int kP = 128 * MT, kRows = (kP + NQ + 31) / 32;
+    constexpr int kRows = (128 + NQ + 31) / 32;
     uint32_t g = 0;
     bool ok = true;
     for (int64_t tile = tile0; tile < tiles && ok; tile += stride) {
-      const int64_t p0 = (tile % p.p_tiles) * kP, q0 = (tile / p.p_tiles) * NQ;
+      const int64_t p0 = (tile % p.p_tiles) * 128, q0 = (tile / p.p_tiles) * NQ;
       for (int k = k0; k < k1 && ok; ++k, ++g) {
-        if ((int)(g % kWarps) != warp - 2) continue;
+        if ((int)(g % kMmScaleWarps) != warp - 2) continue;
         uint2 w[kRows];
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
           const int r = lane + 32 * i;
-          w[i] = r < kP      ? mm_scales(p.p_scale, p0 + r, p.p_rows, p.k32, k, p.wide)
-                 : r < kP + NQ ? mm_scales(p.q_scale, q0 + r - kP, p.q_rows, p.k32, k, p.wide)
-                               : make_uint2(0u, 0u);
+          w[i] = r < 128      ? mm_scales(p.p_scale, p0 + r, p.p_rows, p.k32, k, p.wide)
+                 : r < 128 + NQ ? mm_scales(p.q_scale, q0 + r - 128, p.q_rows, p.k32, k, p.wide)
+                                : make_uint2(0u, 0u);
         }
-        const uint32_t s = g % Sh::stages;
-        if (g >= Sh::stages) ok = role_wait_warp(&sh.empty[s], g / Sh::stages - 1, &sh.abort, p.st);
+        const uint32_t s = g % kMmScaleStages;
+        if (g >= kMmScaleStages) ok = role_wait_warp(&sh.sf_empty[s], g / kMmScaleStages - 1, &sh.abort, p.st);
         if (!ok) break;
-        uint8_t* sf = buf + s * Sh::stage + Sh::codes;
+        uint8_t* sf = buf + Sh::off_scales + s * Sh::scales;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-          const int r = lane + 32 * i, q = r - kP;
-          uint8_t* to = r < kP ? sf + 1024 * (r >> 7) + 16 * (r & 31) + 4 * ((r & 127) >> 5)
-                               : sf + 1024 * MT + 512 * (q >> 7) + 16 * (q & 31) + 4 * ((q & 127) >> 5);
-          if (r < kP + NQ) {
+          const int r = lane + 32 * i, q = r - 128;
+          uint8_t* to = r < 128 ? sf + 16 * (r & 31) + 4 * (r >> 5)
+                                : sf + 1024 + 512 * (q >> 7) + 16 * (q & 31) + 4 * ((q & 127) >> 5);
+          if (r < 128 + NQ) {
             *reinterpret_cast<uint32_t*>(to) = w[i].x;
-            *reinterpret_cast<uint32_t*>(to + (r < kP ? 512 : 512 * Sh::qc)) = w[i].y;
+            *reinterpret_cast<uint32_t*>(to + (r < 128 ? 512 : 512 * Sh::qc)) = w[i].y;
           }
         }
         fence_proxy_async_smem();
@@ -273,22 +276,21 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
     }
   } else {
     // ---------------------------------------------------------------- output
-    // Eight warps: the first four write 128 rows, the others the second 128 of a 256-row tile.  A
-    // split tile's partial goes to shared memory instead ([column][row]; the ring is done with).
-    const int quad = warp & 3, mt = (warp - kMmOutWarp) >> 2;  // the TMEM lanes this warp may read
+    // A split tile's partial goes to shared memory instead ([column][row]; the ring is done with).
+    const int quad = warp & 3;  // the TMEM lanes this warp may read
     const int row_in = quad * 32 + lane;
     constexpr int kStep = NQ < 32 ? 16 : 32;
-    uint8_t* cross = buf + Sh::stage * Sh::stages + (warp - kMmOutWarp) * kMmOutWarp32;
+    uint8_t* cross = buf + Sh::off_out + (warp - kMmOutWarp) * 32 * kMmOutPad;
     const bool wide_out = p.p_is_a && (p.ld * sizeof(T)) % 16 == 0;  // every 8th column is a 16-byte place
     uint32_t n = 0;
-    bool ok = mt < MT;
+    bool ok = true;
     for (int64_t tile = tile0; tile < tiles && ok; tile += stride, ++n) {
-      const int64_t pr = (tile % p.p_tiles) * (MT * 128) + mt * 128 + row_in, q0 = (tile / p.p_tiles) * NQ;
-      const uint32_t ab = n % Sh::accs;
-      ok = role_wait_warp(&sh.acc_full[ab], n / Sh::accs, &sh.abort, p.st);
+      const int64_t pr = (tile % p.p_tiles) * 128 + row_in, q0 = (tile / p.p_tiles) * NQ;
+      const uint32_t ab = n & 1;
+      ok = role_wait_warp(&sh.acc_full[ab], n / 2, &sh.abort, p.st);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t acc = tmem + (MT == 1 ? ab : mt) * Sh::acc_cols + ((uint32_t)(quad * 32) << 16);
+      const uint32_t acc = tmem + ab * Sh::acc_cols + ((uint32_t)(quad * 32) << 16);
 #pragma unroll 1
       for (int c = 0; c < NQ; c += kStep) {
         uint32_t v[kStep];
@@ -336,26 +338,24 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
   if (split > 1) {
     // ---------------------------------------------------------------- a split tile's sum
     // Each CTA adds up its share of the columns over the cluster, in rank order.
-    if constexpr (MT == 1) {
-      __syncwarp();
-      cluster_sync();
-      if (warp >= kMmOutWarp && warp < kMmOutWarp + 4) {
-        const int row_in = (warp - kMmOutWarp) * 32 + lane;
-        const int64_t pr = (tile0 % p.p_tiles) * 128 + row_in, q0 = (tile0 / p.p_tiles) * NQ;
-        const int c0 = NQ * rank / split, c1 = NQ * (rank + 1) / split;
-        for (int c = c0; c < c1; c += 2) {  // NQ / split is 2 at least
-          float f[2] = {0.f, 0.f};
+    __syncwarp();
+    cluster_sync();
+    if (warp >= kMmOutWarp && warp < kMmOutWarp + 4) {
+      const int row_in = (warp - kMmOutWarp) * 32 + lane;
+      const int64_t pr = (tile0 % p.p_tiles) * 128 + row_in, q0 = (tile0 / p.p_tiles) * NQ;
+      const int c0 = NQ * rank / split, c1 = NQ * (rank + 1) / split;
+      for (int c = c0; c < c1; c += 2) {  // NQ / split is 2 at least
+        float f[2] = {0.f, 0.f};
 #pragma unroll
-          for (int r = 0; r < kMmMaxSplit; ++r)
-            if (r < split) {
-              f[0] += ld_cluster_f32(smem_u32(buf) + (c * 128 + row_in) * 4, r);
-              f[1] += ld_cluster_f32(smem_u32(buf) + ((c + 1) * 128 + row_in) * 4, r);
-            }
-          mm_store<2, T>(p, pr, q0 + c, f);
-        }
+        for (int r = 0; r < kMmMaxSplit; ++r)
+          if (r < split) {
+            f[0] += ld_cluster_f32(smem_u32(buf) + (c * 128 + row_in) * 4, r);
+            f[1] += ld_cluster_f32(smem_u32(buf) + ((c + 1) * 128 + row_in) * 4, r);
+          }
+        mm_store<2, T>(p, pr, q0 + c, f);
       }
-      cluster_sync();  // the others may still read this CTA's partial
     }
+    cluster_sync();  // the others may still read this CTA's partial
   }
   pdl_launch_dependents();
   tc_fence_before();
@@ -398,16 +398,16 @@ static bool mm_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MT, int NQ, typename T>
+template <int NQ, typename T>
 static cudaError_t mm_launch_as(const MmParams& p, int sms, cudaStream_t stream) {
-  auto kern = mxfp4_matmul_kernel<MT, NQ, T>;
-  cudaError_t e = ensure_smem(kern, MmShape<MT, NQ>::smem);
+  auto kern = mxfp4_matmul_kernel<NQ, T>;
+  cudaError_t e = ensure_smem(kern, MmShape<NQ>::smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)p.p_tiles * p.q_tiles;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.split > 1 ? tiles * p.split : tiles < sms ? tiles : sms));
   cfg.blockDim = dim3(kMmThreads);
-  cfg.dynamicSmemBytes = MmShape<MT, NQ>::smem;
+  cfg.dynamicSmemBytes = MmShape<NQ>::smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -423,20 +423,20 @@ static cudaError_t mm_launch_as(const MmParams& p, int sms, cudaStream_t stream)
   return e;
 }
 
-template <int MT, int NQ>
+template <int NQ>
 static cudaError_t mm_launch(MmParams& p, const uint8_t* p_codes, const uint8_t* q_codes, int64_t K, int out_dt,
                              int sms, cudaStream_t stream) {
-  p.p_tiles = (int)((p.p_rows + MT * 128 - 1) / (MT * 128));
+  p.p_tiles = (int)((p.p_rows + 127) / 128);
   p.q_tiles = (int)((p.q_rows + NQ - 1) / NQ);
   // few tiles: their inner length is split over a cluster, two steps a CTA at least
   p.split = 1;
-  if (MT == 1 && NQ <= 64)
+  if (NQ <= 64)
     while (p.split < kMmMaxSplit && (int64_t)p.p_tiles * p.q_tiles * p.split * 2 <= sms && p.steps >= 4 * p.split)
       p.split *= 2;
-  if (!mm_map(&p.p_map, p_codes, p.p_rows, K, MT * 128) || !mm_map(&p.q_map, q_codes, p.q_rows, K, NQ))
+  if (!mm_map(&p.p_map, p_codes, p.p_rows, K, 128) || !mm_map(&p.q_map, q_codes, p.q_rows, K, NQ))
     return cudaErrorNotSupported;
-  return out_dt == CSKV_F32 ? mm_launch_as<MT, NQ, float>(p, sms, stream)
-                            : mm_launch_as<MT, NQ, __nv_bfloat16>(p, sms, stream);
+  return out_dt == CSKV_F32 ? mm_launch_as<NQ, float>(p, sms, stream)
+                            : mm_launch_as<NQ, __nv_bfloat16>(p, sms, stream);
 }
 
 cudaError_t launch_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scale, const uint8_t* b_codes,
@@ -458,25 +458,21 @@ cudaError_t launch_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scale, 
   p.out = out;
   p.st = st;
   if (!p.p_is_a)
-    return M <= 16 ? mm_launch<1, 16>(p, pc, qc, K, out_dt, sms, stream)
-           : M <= 32 ? mm_launch<1, 32>(p, pc, qc, K, out_dt, sms, stream)
-                     : mm_launch<1, 64>(p, pc, qc, K, out_dt, sms, stream);
-  // The tile whose waves take the least time, in SM cycles: a step brings a tile's rows (128 bytes
-  // each, at the 28 bytes a cycle that L2 delivers to every SM at once), a tile costs about 400
-  // cycles more, and 10 a column where its output is not hidden (256 rows).
-  int best = 0;
+    return M <= 16 ? mm_launch<16>(p, pc, qc, K, out_dt, sms, stream)
+           : M <= 32 ? mm_launch<32>(p, pc, qc, K, out_dt, sms, stream)
+                     : mm_launch<64>(p, pc, qc, K, out_dt, sms, stream);
+  // the width whose waves of tiles take the least time (a tile costs its columns and a fixed part,
+  // about 64 columns' worth)
+  int best = 192;
   int64_t least = INT64_MAX;
-  for (int nq : {2 * 1000 + 192, 192, 128, 64}) {
-    const int mt = nq / 1000 + (nq < 1000), cols = nq % 1000;
-    const int64_t tiles = ((p.p_rows + 128 * mt - 1) / (128 * mt)) * ((p.q_rows + cols - 1) / cols);
-    const int64_t cost = (tiles + sms - 1) / sms *
-                         (p.steps * (int64_t)((128 * mt + cols) * 128 / 28) + 400 + (mt == 2 ? 10 * cols : 0));
+  for (int nq : {192, 128, 64}) {
+    const int64_t tiles = (int64_t)((p.p_rows + 127) / 128) * ((p.q_rows + nq - 1) / nq);
+    const int64_t cost = (tiles + sms - 1) / sms * (nq + 64);
     if (cost < least) least = cost, best = nq;
   }
-  return best == 2192  ? mm_launch<2, 192>(p, pc, qc, K, out_dt, sms, stream)
-         : best == 192 ? mm_launch<1, 192>(p, pc, qc, K, out_dt, sms, stream)
-         : best == 128 ? mm_launch<1, 128>(p, pc, qc, K, out_dt, sms, stream)
-                       : mm_launch<1, 64>(p, pc, qc, K, out_dt, sms, stream);
+  return best == 192   ? mm_launch<192>(p, pc, qc, K, out_dt, sms, stream)
+         : best == 128 ? mm_launch<128>(p, pc, qc, K, out_dt, sms, stream)
+                       : mm_launch<64>(p, pc, qc, K, out_dt, sms, stream);
 }
 
 }  // namespace cskv
