@@ -24,7 +24,6 @@ constexpr int kMmThreads = 320;          // warp 0 TMA, 1 products, 2-5 scales, 
 constexpr int kMmScaleWarps = 4, kMmOutWarp = 2 + kMmScaleWarps;
 constexpr int kMmDeep = 256;             // codes of a stage: 128 bytes a row
 constexpr uint32_t kMmTileP = 128 * 128;  // bytes of P's 128 rows of codes
-constexpr int kMmScaleStages = 8;        // a multiple of the scale warps: each meets its own stages in order
 constexpr uint32_t kMmOutPad = 144;      // bytes of a staged output row: 128 and a skew of four banks
 constexpr int kMmMaxSplit = 8;           // CTAs of a cluster that share a tile's inner length
 
@@ -48,7 +47,7 @@ struct MmShape {
   static constexpr uint32_t codes = kMmTileP + NQ * 128u;    // a stage's code bytes
   static constexpr uint32_t scales = 1024u * (1 + qc);       // a step's scales: two K chunks each
   static constexpr int stages = (int)(163840u / codes) < 8 ? (int)(163840u / codes) : 8;
-  static constexpr uint32_t off_scales = codes * stages, off_out = off_scales + scales * kMmScaleStages;
+  static constexpr uint32_t off_scales = codes * stages, off_out = off_scales + scales * stages;
   static constexpr size_t smem = off_out + 4 * 32 * kMmOutPad + 1024;
   static constexpr int acc_cols = NQ < 32 ? 32 : NQ;         // TMEM columns of an accumulator
   // a step's scales in TMEM: when those of step g + 1 are copied, step g's codes are there, so the
@@ -61,7 +60,7 @@ struct MmShape {
 };
 
 struct MmShared {
-  uint64_t full[8], empty[8], sf_full[kMmScaleStages], sf_empty[kMmScaleStages], acc_full[2], acc_empty[2], bail;
+  uint64_t full[8], empty[8], first, acc_full[2], acc_empty[2], bail;
   uint32_t tmem;
   int abort;
 };
@@ -119,8 +118,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
   __shared__ MmShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t tiles = (int64_t)p.p_tiles * p.q_tiles;
-  // this CTA's part of its tiles' inner length
-  const int split = p.split, rank = split > 1 ? (int)cluster_rank() : 0;
+  // this CTA's part of its tiles' inner length (its rank in a one-dimensional cluster)
+  const int split = p.split, rank = (int)(blockIdx.x % (unsigned)split);
   const int64_t tile0 = blockIdx.x / split, stride = gridDim.x / split;
   const int k0 = (int)((int64_t)p.steps * rank / split), k1 = (int)((int64_t)p.steps * (rank + 1) / split);
 
@@ -134,13 +133,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
   }
   if (tid == 0) {
     for (int i = 0; i < Sh::stages; ++i) {
-      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.full[i], 2);
       mbar_init(&sh.empty[i], 1);
     }
-    for (int i = 0; i < kMmScaleStages; ++i) {
-      mbar_init(&sh.sf_full[i], 1);
-      mbar_init(&sh.sf_empty[i], 1);
-    }
+    mbar_init(&sh.first, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.acc_full[i], 1);
       mbar_init(&sh.acc_empty[i], 4);
@@ -183,36 +179,39 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
     // A step's descriptors differ by their address field alone (16-byte units).
     const uint32_t base = smem_u32(buf);
     const uint64_t d_codes = smem_desc_sw128(base, 16, 1024), d_scales = smem_desc_noswz(base + Sh::off_scales, 16, 128);
-    uint32_t n = 0, s = 0, sp = 0;              // tiles; stage and phase of the codes
-    uint32_t ss = 0, ssp = 0, sb = 0, pb = 0;   // stage and phase of the scales; TMEM buffer of the copies, of the products
-    uint32_t st = 0;                            // scale stage of the products
-    bool ok = true;
+    uint32_t n = 0, s = 0, sp = 0;  // tiles; stage and phase of a step
+    uint32_t ss = 0, sb = 0, pb = 0;  // scales' stage; TMEM buffer of the copies, of the products
+    // A wait that gave up does not end the loops: what decides them has to be uniform for the compiler,
+    // or every operand is moved to a uniform register at each use (which took longer than the
+    // products).  The products then run on what is there, and the call is flagged.
     // Scales of a step -> tensor memory, 512 bytes a chunk of 128 rows and 4 K scales: P's two K chunks,
     // then Q's rows by K chunk.
     auto copy_scales = [&]() {
-      if (!role_wait_warp(&sh.sf_full[ss], ssp, &sh.abort, p.st)) return false;
-      tc_fence_after();
       if (elect_one()) {
 #pragma unroll
         for (int i = 0; i < 2 * (1 + Sh::qc); ++i)
           tc_cp_scales(tmem + Sh::sf_col + sb * Sh::sf_step + 4 * i, d_scales + ss * (Sh::scales >> 4) + 32 * i);
       }
-      __syncwarp();
-      if (++ss == kMmScaleStages) ss = 0, ssp ^= 1;
+      if (++ss == Sh::stages) ss = 0;
       if (++sb == Sh::sf_bufs) sb = 0;
-      return true;
     };
-    for (int64_t tile = tile0; tile < tiles && ok; tile += stride, ++n) {
+    if (tile0 < tiles) {
+      role_wait(&sh.first, 0, &sh.abort, p.st);
+      __syncwarp();
+      tc_fence_after();
+      copy_scales();
+      __syncwarp();
+    }
+    for (int64_t tile = tile0; tile < tiles; tile += stride, ++n) {
       const uint32_t ab = n & 1;
-      if (n >= 2) ok = role_wait_warp(&sh.acc_empty[ab], n / 2 - 1, &sh.abort, p.st);
-      for (int k = k0; k < k1 && ok; ++k) {
-        ok = role_wait_warp(&sh.full[s], sp, &sh.abort, p.st);
+      if (n >= 2) role_wait(&sh.acc_empty[ab], n / 2 - 1, &sh.abort, p.st);
+      for (int k = k0; k < k1; ++k) {
+        role_wait(&sh.full[s], sp, &sh.abort, p.st);
+        __syncwarp();
+        tc_fence_after();
         // a step's scales go out before the products of the step before it, which need not wait for
         // them then
-        if (ok && k == k0) ok = copy_scales();
-        if (ok && k + 1 < k1) ok = copy_scales();
-        if (!ok) break;
-        tc_fence_after();
+        if (k + 1 < k1 || tile + stride < tiles) copy_scales();
         const uint32_t col = tmem + Sh::sf_col + pb * Sh::sf_step;
         const uint64_t d = d_codes + s * (Sh::codes >> 4);
         if (elect_one()) {
@@ -221,28 +220,35 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
             tc_mma_mxf4(tmem + ab * Sh::acc_cols, d + 2 * kk, d + (kMmTileP >> 4) + 2 * kk,
                         idesc_mxf4(128, NQ, 2 * (kk & 1)), col + 4 * (kk >> 1), col + 8 + 4 * Sh::qc * (kk >> 1),
                         k > k0 || kk > 0);
-          tc_commit(&sh.empty[s]);
-          tc_commit(&sh.sf_empty[st]);
+          tc_commit(&sh.empty[s]);  // and the scales of the next step are copied
           if (k + 1 == k1) tc_commit(&sh.acc_full[ab]);
         }
         __syncwarp();
         if (++s == Sh::stages) s = 0, sp ^= 1;
-        if (++st == kMmScaleStages) st = 0;
         if (++pb == Sh::sf_bufs) pb = 0;
       }
     }
-    if (!ok && elect_one()) {  // gave up: nothing of this CTA may still be in flight when its memory is released
+    if (elect_one()) {  // nothing of this CTA may still be in flight when its memory is released
       tc_commit(&sh.bail);
       mbar_wait_bounded(&sh.bail, 0);
     }
     __syncwarp();
   } else if (warp < kMmOutWarp) {
     // ---------------------------------------------------------------- scales
-    // Warp w takes every fourth step.  A row's eight bytes are two words, one for each 512-byte
+    // Warp w takes every fourth step.  A step's scales are counted with the codes of the step before
+    // it, which is when they are copied on, so that a step of the products has one wait and one commit
+    // (a wait and a commit took about 100 cycles each of 880; the products of a step take 390).  A row's eight bytes are two words, one for each 512-byte
     // chunk of 128 rows x 4 K scales: row r at 16 (r % 32) + 4 (r / 32).
     constexpr int kRows = (128 + NQ + 31) / 32;
     uint32_t g = 0;
     bool ok = true;
+    // step g - 1 - stages is complete: its stage of `full` may be counted for step g - 1, and step
+    // g - stages' scales, copied before its products, have left their place (step 0's before step 0's)
+    auto room = [&](uint32_t at) {
+      if (at < (uint32_t)Sh::stages) return true;
+      const uint32_t h = at == (uint32_t)Sh::stages ? 0 : at - 1 - Sh::stages;
+      return role_wait_warp(&sh.empty[h % Sh::stages], h / Sh::stages, &sh.abort, p.st);
+    };
     for (int64_t tile = tile0; tile < tiles && ok; tile += stride) {
       const int64_t p0 = (tile % p.p_tiles) * 128, q0 = (tile / p.p_tiles) * NQ;
       for (int k = k0; k < k1 && ok; ++k, ++g) {
@@ -255,10 +261,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
                  : r < 128 + NQ ? mm_scales(p.q_scale, q0 + r - 128, p.q_rows, p.k32, k, p.wide)
                                 : make_uint2(0u, 0u);
         }
-        const uint32_t s = g % kMmScaleStages;
-        if (g >= kMmScaleStages) ok = role_wait_warp(&sh.sf_empty[s], g / kMmScaleStages - 1, &sh.abort, p.st);
-        if (!ok) break;
-        uint8_t* sf = buf + Sh::off_scales + s * Sh::scales;
+        if (!(ok = room(g))) break;
+        uint8_t* sf = buf + Sh::off_scales + g % Sh::stages * Sh::scales;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
           const int r = lane + 32 * i, q = r - 128;
@@ -271,9 +275,12 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.sf_full[s]);
+        if (lane == 0) mbar_arrive(g ? &sh.full[(g - 1) % Sh::stages] : &sh.first);
       }
     }
+    // the last step has no successor
+    if (ok && g && (int)(g % kMmScaleWarps) == warp - 2 && room(g) && lane == 0)
+      mbar_arrive(&sh.full[(g - 1) % Sh::stages]);
   } else {
     // ---------------------------------------------------------------- output
     // A split tile's partial goes to shared memory instead ([column][row]; the ring is done with).
