@@ -35,7 +35,7 @@ struct MmParams {
   int p_tiles, q_tiles, steps;
   int split;                    // CTAs that share a tile (the size of the cluster)
   int p_is_a;                   // out[p, q] (P rows are a's), else out[q, p]
-  int wide;                     // bytes of a scale load: 8, 4 or 1
+  int wide;                     // bytes of a scale load: 32, 4 or 1
   void* out;
   int* st;
 };
@@ -65,25 +65,29 @@ struct MmShared {
   int abort;
 };
 
-// Scale bytes 8 step .. 8 step + 7 of a row, zeros past its end or for a row that is not there.
-__device__ __forceinline__ uint2 mm_scales(const uint8_t* scale, int64_t row, int64_t rows, int64_t k32, int step,
-                                           int wide) {
-  uint2 w = make_uint2(0u, 0u);
-  if (row < rows) {
-    const uint8_t* s = scale + row * k32 + 8 * (int64_t)step;
-    const int left = (int)min((int64_t)8, k32 - 8 * (int64_t)step);
-    if (wide == 8) {
-      w = __ldg(reinterpret_cast<const uint2*>(s));
-    } else if (wide == 4) {
-      w.x = __ldg(reinterpret_cast<const uint32_t*>(s));
-      if (left > 4) w.y = __ldg(reinterpret_cast<const uint32_t*>(s) + 1);
-    } else {
+// Scale bytes of steps k .. end - 1 of a row, which lie in one aligned group of four steps (32 bytes,
+// one sector), at their places in the group.  Zeros past the row's end or for a row that is not there.
+__device__ __forceinline__ void mm_scales(const uint8_t* scale, int64_t row, int64_t rows, int64_t k32, int k, int end,
+                                          int wide, uint32_t (&w)[8]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) (i < 4 ? w.x : w.y) |= (uint32_t)__ldg(s + i) << (8 * (i & 3));
-    }
+  for (int i = 0; i < 8; ++i) w[i] = 0u;
+  if (row >= rows) return;
+  const int64_t at = 8 * (int64_t)(k & ~3);
+  const uint8_t* s = scale + row * k32 + at;
+  const int from = 8 * (k & 3), to = (int)min(8 * (int64_t)end, k32) - (int)at;
+  if (wide == 32) {
+    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+        : "l"(s));
+  } else if (wide == 4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (4 * i >= from && 4 * i < to) w[i] = __ldg(reinterpret_cast<const uint32_t*>(s) + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i >= from && i < to) w[i >> 2] |= (uint32_t)__ldg(s + i) << (8 * (i & 3));
   }
-  return w;
 }
 
 // Columns q .. q + STEP - 1 of row `pr` of a tile.
@@ -133,10 +137,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
   }
   if (tid == 0) {
     for (int i = 0; i < Sh::stages; ++i) {
-      mbar_init(&sh.full[i], 2);
+      mbar_init(&sh.full[i], 1 + kMmScaleWarps);
       mbar_init(&sh.empty[i], 1);
     }
-    mbar_init(&sh.first, 1);
+    mbar_init(&sh.first, kMmScaleWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.acc_full[i], 1);
       mbar_init(&sh.acc_empty[i], 4);
@@ -235,13 +239,26 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
     __syncwarp();
   } else if (warp < kMmOutWarp) {
     // ---------------------------------------------------------------- scales
-    // Warp w takes every fourth step.  A step's scales are counted with the codes of the step before
-    // it, which is when they are copied on, so that a step of the products has one wait and one commit
-    // (a wait and a commit took about 100 cycles each of 880; the products of a step take 390).  A row's eight bytes are two words, one for each 512-byte
-    // chunk of 128 rows x 4 K scales: row r at 16 (r % 32) + 4 (r / 32).
-    constexpr int kRows = (128 + NQ + 31) / 32;
-    uint32_t g = 0;
-    bool ok = true;
+    // Warp w takes every fourth group of 32 rows, four steps at a time (a row's 32 bytes, the next
+    // four on their way).  A step's eight bytes are two words, one for each 512-byte chunk of
+    // 128 rows x 4 K scales: row r at 16 (r % 32) + 4 (r / 32).  A step's scales are counted with the
+    // codes of the step before it, which is when they are copied on, so that a step of the products
+    // has one wait and one commit.
+    constexpr int kGroups = 4 + (NQ + 31) / 32, kMine = (kGroups + kMmScaleWarps - 1) / kMmScaleWarps;
+    const int w0 = warp - 2;
+    uint32_t cur[kMine][8], nxt[kMine][8];
+    auto load = [&](int64_t tile, int k, uint32_t (&w)[kMine][8]) {
+      const int64_t p0 = (tile % p.p_tiles) * 128, q0 = (tile / p.p_tiles) * NQ;
+      const int end = min((k & ~3) + 4, k1);
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int r = 32 * (w0 + kMmScaleWarps * i) + lane;
+        if (i == 0)  // P's four groups
+          mm_scales(p.p_scale, p0 + r, p.p_rows, p.k32, k, end, p.wide, w[i]);
+        else
+          mm_scales(p.q_scale, r < 128 + NQ ? q0 + r - 128 : p.q_rows, p.q_rows, p.k32, k, end, p.wide, w[i]);
+      }
+    };
     // step g - 1 - stages is complete: its stage of `full` may be counted for step g - 1, and step
     // g - stages' scales, copied before its products, have left their place (step 0's before step 0's)
     auto room = [&](uint32_t at) {
@@ -249,38 +266,44 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
       const uint32_t h = at == (uint32_t)Sh::stages ? 0 : at - 1 - Sh::stages;
       return role_wait_warp(&sh.empty[h % Sh::stages], h / Sh::stages, &sh.abort, p.st);
     };
-    for (int64_t tile = tile0; tile < tiles && ok; tile += stride) {
-      const int64_t p0 = (tile % p.p_tiles) * 128, q0 = (tile / p.p_tiles) * NQ;
-      for (int k = k0; k < k1 && ok; ++k, ++g) {
-        if ((int)(g % kMmScaleWarps) != warp - 2) continue;
-        uint2 w[kRows];
+    uint32_t g = 0;
+    bool ok = true;
+    int64_t tile = tile0;
+    int k = k0;
+    if (tile < tiles) load(tile, k, cur);
+    while (tile < tiles && ok) {
+      const int base = k & ~3, end = min(base + 4, k1);
+      const int64_t next_tile = end < k1 ? tile : tile + stride;
+      const int next_k = end < k1 ? end : k0;
+      if (next_tile < tiles) load(next_tile, next_k, nxt);
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const int r = lane + 32 * i;
-          w[i] = r < 128      ? mm_scales(p.p_scale, p0 + r, p.p_rows, p.k32, k, p.wide)
-                 : r < 128 + NQ ? mm_scales(p.q_scale, q0 + r - 128, p.q_rows, p.k32, k, p.wide)
-                                : make_uint2(0u, 0u);
-        }
-        if (!(ok = room(g))) break;
-        uint8_t* sf = buf + Sh::off_scales + g % Sh::stages * Sh::scales;
+      for (int j = 0; j < 4; ++j) {
+        if (base + j < k || base + j >= end || !ok) continue;
+        if (!(ok = room(g))) continue;
+        uint8_t* sf = buf + Sh::off_scales + g % Sh::stages * Sh::scales + 16 * lane;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const int r = lane + 32 * i, q = r - 128;
-          uint8_t* to = r < 128 ? sf + 16 * (r & 31) + 4 * (r >> 5)
-                                : sf + 1024 + 512 * (q >> 7) + 16 * (q & 31) + 4 * ((q & 127) >> 5);
-          if (r < 128 + NQ) {
-            *reinterpret_cast<uint32_t*>(to) = w[i].x;
-            *reinterpret_cast<uint32_t*>(to + (r < 128 ? 512 : 512 * Sh::qc)) = w[i].y;
+        for (int i = 0; i < kMine; ++i) {
+          const int q = 32 * (w0 + kMmScaleWarps * (i - 1));  // Q's rows of this group
+          uint8_t* to = i == 0 ? sf + 4 * w0 : sf + 1024 + 512 * (q >> 7) + 4 * ((q & 127) >> 5);
+          if (i == 0 || q + lane < NQ) {
+            *reinterpret_cast<uint32_t*>(to) = cur[i][2 * j];
+            *reinterpret_cast<uint32_t*>(to + (i == 0 ? 512 : 512 * Sh::qc)) = cur[i][2 * j + 1];
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(g ? &sh.full[(g - 1) % Sh::stages] : &sh.first);
+        ++g;
       }
+#pragma unroll
+      for (int i = 0; i < kMine; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) cur[i][j] = nxt[i][j];
+      tile = next_tile;
+      k = next_k;
     }
     // the last step has no successor
-    if (ok && g && (int)(g % kMmScaleWarps) == warp - 2 && room(g) && lane == 0)
-      mbar_arrive(&sh.full[(g - 1) % Sh::stages]);
+    if (ok && g && room(g) && lane == 0) mbar_arrive(&sh.full[(g - 1) % Sh::stages]);
   } else {
     // ---------------------------------------------------------------- output
     // A split tile's partial goes to shared memory instead ([column][row]; the ring is done with).
@@ -461,7 +484,7 @@ cudaError_t launch_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scale, 
   p.ld = N;
   p.steps = (int)((K + kMmDeep - 1) / kMmDeep);
   const uintptr_t places = (uintptr_t)a_scale | (uintptr_t)b_scale | (uintptr_t)p.k32;
-  p.wide = places % 8 == 0 ? 8 : places % 4 == 0 ? 4 : 1;
+  p.wide = places % 32 == 0 ? 32 : places % 4 == 0 ? 4 : 1;
   p.out = out;
   p.st = st;
   if (!p.p_is_a)
