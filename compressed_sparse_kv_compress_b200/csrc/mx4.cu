@@ -5,6 +5,10 @@
 // neighbouring values (16 or 32 bytes a load), so four lanes hold a block: its largest magnitude
 // is two shuffles (compared as integers: the order of non-negative floats, and an infinity or a
 // NaN stays the largest), and a warp's loads and code stores are contiguous.
+// (Sixteen values a lane halve the shuffles, but the loads were no longer contiguous: slower.)
+// Measured, quantised and back: 262144 x 64 bf16, 85 MB in 15.0 us, 5.65 TB/s, 0.86 of the copy rate;
+// 262144 main-KV rows from bf16, 361 MB in 75 us, 4.8 TB/s, 0.73 (issue active 68 % of the cycles);
+// a few rows: the latency of two launches, 2.1 us.
 #include "launch.cuh"
 #include "mx4.cuh"
 

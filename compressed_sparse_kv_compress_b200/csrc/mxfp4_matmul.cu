@@ -4,15 +4,21 @@
 // [SW] shareware.cn/news/167317 §六.1 (FP4 suffices for ranking): rows of E2M1 codes with one E8M0
 // scale per 32 values (mx4.cuh), exact products, fp32 accumulation.
 //
-// Large products are bound by the tensor pipe (a 128 x 192 tile's step is four products of about 200
-// cycles; its 41 KB arrive in less), a few rows by the latency of a step, so few tiles are split
-// over the inner length inside a thread-block cluster.  A persistent CTA an SM, with roles: one
-// thread loads code tiles by TMA (128-byte swizzle, 256 codes deep, zeros past the edges), four
-// warps load the rows' scales and lay them out as the tensor core wants them, one warp copies
-// scales to tensor memory and issues the products, four warps write out a tile while the next
-// one's products run (two accumulators).  Codes and scales have rings of their own: in one ring a
-// step waited for the slower of the two (4096^3: 50 us).  The 128-row operand P is a, or, for a few
-// rows of a, b: the tile is then as narrow as those rows.
+// A persistent CTA an SM, with roles: one thread loads code tiles by TMA (128-byte swizzle, 256 codes
+// deep, zeros past the edges), four warps load the rows' scales and lay them out as the tensor core
+// wants them, one warp copies scales to tensor memory and issues the products, four warps write
+// out a tile while the next one's products run (two accumulators).  The 128-row operand P is a,
+// or, for a few rows of a, b: the tile is then as narrow as those rows, and few tiles are split over
+// the inner length inside a thread-block cluster, since one step is a chain of latencies.
+//
+// What bounds it: a step (256 deep) of a 128 x 192 tile is four products of about 95 cycles, its
+// 41 KB take 640 at the 64 bytes a cycle that an SM reads from L2, and issuing it takes about 650
+// (a wait 80, six scale copies 150-200, the products 100, the commit 230), so the tensor pipe is
+// active for 44 % of the cycles.  Steps that count here: scales copied a step before their products
+// (4096^3: 50.5 -> 46.4 us), one wait and one commit a step (41.0), a row's scales loaded one
+// sector, four steps, at a time (38.2).
+// Measured (device time): 4096^3, bf16 out: 38 us, 3.6 PFLOP/s; 4096 x 512 x 4096: 10.3 us; one row
+// x 4096 x 4096: 5.5 us, 1.6 TB/s of codes; 67 x 1000 x 2080: 9.9 us.
 #include <cuda.h>
 
 #include "launch.cuh"
@@ -35,7 +41,7 @@ struct MmParams {
   int p_tiles, q_tiles, steps;
   int split;                    // CTAs that share a tile (the size of the cluster)
   int p_is_a;                   // out[p, q] (P rows are a's), else out[q, p]
-  int wide;                     // bytes of a scale load: 32, 4 or 1
+  int wide;                     // alignment of every row's scales: 32, 16, 8, 4 or 1 bytes
   void* out;
   int* st;
 };
@@ -67,6 +73,9 @@ struct MmShared {
 
 // Scale bytes of steps k .. end - 1 of a row, which lie in one aligned group of four steps (32 bytes,
 // one sector), at their places in the group.  Zeros past the row's end or for a row that is not there.
+// `wide`: the alignment of all rows, the widest load of which serves (the lanes' rows are all in
+// different sectors, so a load costs 32 lookups; 4096^3 by 32 / 16 / 8 / 4 / 1 bytes: 38 / 40 / 43 / 53 /
+// 90 us; by single bytes 171).
 __device__ __forceinline__ void mm_scales(const uint8_t* scale, int64_t row, int64_t rows, int64_t k32, int k, int end,
                                           int wide, uint32_t (&w)[8]) {
 #pragma unroll
@@ -79,14 +88,46 @@ __device__ __forceinline__ void mm_scales(const uint8_t* scale, int64_t row, int
     asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
         : "l"(s));
+  } else if (wide == 16) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4)
+      if (4 * i + 16 > from && 4 * i < to) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(s + 4 * i));
+        w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+      }
+  } else if (wide == 8) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+      if (4 * i >= from && 4 * i < to) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(s + 4 * i));
+        w[i] = v.x, w[i + 1] = v.y;
+      }
   } else if (wide == 4) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (4 * i >= from && 4 * i < to) w[i] = __ldg(reinterpret_cast<const uint32_t*>(s) + i);
   } else {
+    // rows that begin anywhere: the aligned words around them (by bytes where such a word reaches out
+    // of the matrix), shifted into place; what follows the row is cut off
+    const int a = (int)(reinterpret_cast<uintptr_t>(s) & 3);
+    const uint8_t* last = scale + rows * k32;
+    uint32_t v[9];
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i >= from && i < to) w[i >> 2] |= (uint32_t)__ldg(s + i) << (8 * (i & 3));
+    for (int i = 0; i < 9; ++i) {
+      const uint8_t* at4 = s - a + 4 * i;
+      v[i] = 0u;
+      if (4 * i + 4 <= a + from || 4 * i >= a + to) continue;
+      if (at4 >= scale && at4 + 4 <= last)
+        v[i] = __ldg(reinterpret_cast<const uint32_t*>(at4));
+      else
+        for (int j = 0; j < 4; ++j)
+          if (at4 + j >= scale && at4 + j < last) v[i] |= (uint32_t)__ldg(at4 + j) << (8 * j);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[i] = __funnelshift_r(v[i], v[i + 1], 8 * a);
+      if (4 * i + 4 > to) w[i] &= 4 * i < to ? (1u << (8 * (to & 3))) - 1u : 0u;
+    }
   }
 }
 
@@ -484,7 +525,7 @@ cudaError_t launch_mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scale, 
   p.ld = N;
   p.steps = (int)((K + kMmDeep - 1) / kMmDeep);
   const uintptr_t places = (uintptr_t)a_scale | (uintptr_t)b_scale | (uintptr_t)p.k32;
-  p.wide = places % 32 == 0 ? 32 : places % 4 == 0 ? 4 : 1;
+  p.wide = places % 32 == 0 ? 32 : places % 16 == 0 ? 16 : places % 8 == 0 ? 8 : places % 4 == 0 ? 4 : 1;
   p.out = out;
   p.st = st;
   if (!p.p_is_a)

@@ -164,3 +164,21 @@ def test_empty_and_refusals():
         api.mxfp4_matmul(z(3, 32), z(3, 2), z(4, 32), z(4, 2), torch.empty(3, 4, dtype=torch.float16, device="cuda"))
     with pytest.raises(CskvError):
         api.mxfp4_matmul(z(3, 8), z(3, 0), z(4, 8), z(4, 0))     # half a block
+
+
+@pytest.mark.parametrize("at", [0, 1, 2, 3, 4, 8, 16, 32])
+@pytest.mark.parametrize("M,N,K", [(5, 70, 96), (40, 200, 2080), (70, 130, 1056), (200, 300, 1152), (130, 200, 1312),
+                                   (300, 400, 1280), (513, 200, 1536), (1, 129, 4096)])
+def test_every_alignment_of_the_scales(M, N, K, at):
+    # scales from `at` bytes into a buffer whose other bytes are NaN scales: one of them in a product
+    # would show in every output of its row
+    rng = np.random.default_rng(M + K)
+    (ac, as_, a), (bc, bs, b) = _mat(rng, M, K, 3), _mat(rng, N, K, 3)
+
+    def shifted(s):
+        pad = torch.full((s.numel() + 96,), 0xFF, dtype=torch.uint8, device="cuda")
+        v = pad[at:at + s.numel()].view(s.shape)
+        v.copy_(s)
+        return v
+
+    _check(api.mxfp4_matmul(ac, shifted(as_), bc, shifted(bs), dtype=torch.float32), a, b)
