@@ -35,7 +35,9 @@ def _dt(t) -> int:
 
 def _check(fn: str, *specs) -> None:
     """Refuses tensors that `fn` cannot take.  specs: (name, tensor or None, dtypes, shape); all of
-    them have to be contiguous and on the current CUDA device, whose stream the call runs on."""
+    them have to be contiguous and on the current CUDA device, whose stream the call runs on.
+    Outputs that the call allocates itself come after it, unchecked: for a few rows a call's time
+    is the host's."""
     dev = torch.cuda.current_device()
     for name, t, dtypes, shape in specs:
         if t is None:
@@ -54,6 +56,13 @@ _U8 = (torch.uint8,)
 _I64 = (torch.int64,)
 _I32 = (torch.int32,)
 _VALUES = (torch.float32, torch.bfloat16)
+
+
+def _new(fn, shape, dtype, dtypes, device):
+    """An output of the call's own."""
+    if dtype not in dtypes:
+        raise ValueError(f"{fn}: dtype {dtype}")
+    return torch.empty(*shape, dtype=dtype, device=device)  # the sizes one by one: 1 us less than as a tuple
 
 
 def _stream(stream) -> int:
@@ -258,11 +267,11 @@ def mxfp4_quantize(x, codes=None, bscale=None, *, stream=None):
     E2M1 codes a byte, bscale [..., D/32] uint8, one E8M0 scale per 32 values)."""
     *lead, D = x.shape
     cs, bs = _mxfp4_shapes("mxfp4_quantize", lead, D)
-    if codes is None:
-        codes = torch.empty(cs, dtype=torch.uint8, device=x.device)
-    if bscale is None:
-        bscale = torch.empty(bs, dtype=torch.uint8, device=x.device)
     _check("mxfp4_quantize", ("x", x, _VALUES, x.shape), ("codes", codes, _U8, cs), ("bscale", bscale, _U8, bs))
+    if codes is None:
+        codes = _new("mxfp4_quantize", cs, torch.uint8, _U8, x.device)
+    if bscale is None:
+        bscale = _new("mxfp4_quantize", bs, torch.uint8, _U8, x.device)
     st = _lib.load().mxfp4_quantize(x.data_ptr(), _DT[x.dtype], x.numel() // D, D, codes.data_ptr(),
                                     bscale.data_ptr(), _stream(stream))
     _lib.check("mxfp4_quantize", st)
@@ -274,10 +283,10 @@ def mxfp4_dequantize(codes, bscale, out=None, *, dtype=torch.bfloat16, stream=No
     *lead, half = codes.shape
     D = 2 * half
     _, bs = _mxfp4_shapes("mxfp4_dequantize", lead, D)
-    if out is None:
-        out = torch.empty((*lead, D), dtype=dtype, device=codes.device)
     _check("mxfp4_dequantize", ("codes", codes, _U8, codes.shape), ("bscale", bscale, _U8, bs),
            ("out", out, _VALUES, (*lead, D)))
+    if out is None:
+        out = _new("mxfp4_dequantize", (*lead, D), dtype, _VALUES, codes.device)
     st = _lib.load().mxfp4_dequantize(codes.data_ptr(), bscale.data_ptr(), out.numel() // D, D, _DT[out.dtype],
                                       out.data_ptr(), _stream(stream))
     _lib.check("mxfp4_dequantize", st)
@@ -288,11 +297,11 @@ def mxfp4_matmul(a_codes, a_bscale, b_codes, b_bscale, out=None, *, dtype=torch.
     """out [M, N] = a b^T of MXFP4 matrices (mxfp4_quantize): a_codes [M, K/2], a_bscale [M, K/32],
     b_codes [N, K/2], b_bscale [N, K/32]; out fp32 or bf16 (`dtype`, or out's)."""
     (M, half), (N, _) = a_codes.shape, b_codes.shape
-    if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=a_codes.device)
     _check("mxfp4_matmul", ("a_codes", a_codes, _U8, (M, half)), ("a_bscale", a_bscale, _U8, (M, half // 16)),
            ("b_codes", b_codes, _U8, (N, half)), ("b_bscale", b_bscale, _U8, (N, half // 16)),
            ("out", out, _VALUES, (M, N)), ("dev_status", dev_status, _I32, (1,)))
+    if out is None:
+        out = _new("mxfp4_matmul", (M, N), dtype, _VALUES, a_codes.device)
     st = _lib.load().mxfp4_matmul(a_codes.data_ptr(), a_bscale.data_ptr(), b_codes.data_ptr(), b_bscale.data_ptr(),
                                   M, N, 2 * half, _DT[out.dtype], out.data_ptr(), _ptr(dev_status), _stream(stream))
     _lib.check("mxfp4_matmul", st)
@@ -304,13 +313,13 @@ def kv_quantize_fp4(rows, out=None, *, dst=None, dev_status=None, stream=None):
     int64: row i goes to out[dst[i]] (negative: left out; no two equal); None: to out[i].  Rows of
     `out` that are not named stay as they were."""
     n = rows.shape[0]
-    if out is None:
-        if dst is not None:
-            raise ValueError("kv_quantize_fp4: dst needs the cache it points into (out)")
-        out = torch.empty((n, KV4_ROW_BYTES), dtype=torch.uint8, device=rows.device)
-    cap = out.shape[0]
+    if out is None and dst is not None:
+        raise ValueError("kv_quantize_fp4: dst needs the cache it points into (out)")
+    cap = out.shape[0] if out is not None else n
     _check("kv_quantize_fp4", ("rows", rows, _VALUES, (n, 256)), ("out", out, _U8, (cap, KV4_ROW_BYTES)),
            ("dst", dst, _I64, (n,)), ("dev_status", dev_status, _I32, (1,)))
+    if out is None:
+        out = _new("kv_quantize_fp4", (n, KV4_ROW_BYTES), torch.uint8, _U8, rows.device)
     st = _lib.load().kv_quantize_fp4(rows.data_ptr(), _DT[rows.dtype], n, _ptr(dst), cap, out.data_ptr(),
                                      _ptr(dev_status), _stream(stream))
     _lib.check("kv_quantize_fp4", st)
@@ -322,10 +331,10 @@ def kv_dequantize_fp4(cache, out=None, *, src=None, dtype=torch.bfloat16, dev_st
     src [n] int64 of it (negative: zeros), or its first rows (all of them without `out`)."""
     cap = cache.shape[0]
     n = src.shape[0] if src is not None else out.shape[0] if out is not None else cap
-    if out is None:
-        out = torch.empty((n, 256), dtype=dtype, device=cache.device)
     _check("kv_dequantize_fp4", ("cache", cache, _U8, (cap, KV4_ROW_BYTES)), ("out", out, _VALUES, (n, 256)),
            ("src", src, _I64, (n,)), ("dev_status", dev_status, _I32, (1,)))
+    if out is None:
+        out = _new("kv_dequantize_fp4", (n, 256), dtype, _VALUES, cache.device)
     st = _lib.load().kv_dequantize_fp4(cache.data_ptr(), _ptr(src), cap, n, _DT[out.dtype], out.data_ptr(),
                                        _ptr(dev_status), _stream(stream))
     _lib.check("kv_dequantize_fp4", st)
