@@ -33,9 +33,9 @@ def _dt(t) -> int:
         raise ValueError(f"unsupported dtype {t.dtype}") from None
 
 
-def _check(fn: str, *specs) -> None:
+def _check(fn: str, *specs) -> int:
     """Refuses tensors that `fn` cannot take.  specs: (name, tensor or None, dtypes, shape); all of
-    them have to be contiguous and on the current CUDA device, whose stream the call runs on.
+    them have to be contiguous and on the current CUDA device (returned), whose stream the call runs on.
     Outputs that the call allocates itself come after it, unchecked: for a few rows a call's time
     is the host's."""
     dev = torch.cuda.current_device()
@@ -50,6 +50,7 @@ def _check(fn: str, *specs) -> None:
             raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{fn}: {name} is not contiguous")
+    return dev
 
 
 _U8 = (torch.uint8,)
@@ -65,11 +66,11 @@ def _new(fn, shape, dtype, dtypes, device):
     return torch.empty(*shape, dtype=dtype, device=device)  # the sizes one by one: 1 us less than as a tuple
 
 
-def _stream(stream) -> int:
+def _stream(stream, dev=None) -> int:
     if stream is not None:
         return stream.cuda_stream
     # the handle alone: building torch's stream object costs 3 us a call
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
 
 
 def csa_compress(x_a, z_a, x_b, z_b, tok_off, ent_off, out, *, max_blocks, bias_a=None, bias_b=None, tok0=None,
@@ -267,13 +268,13 @@ def mxfp4_quantize(x, codes=None, bscale=None, *, stream=None):
     E2M1 codes a byte, bscale [..., D/32] uint8, one E8M0 scale per 32 values)."""
     *lead, D = x.shape
     cs, bs = _mxfp4_shapes("mxfp4_quantize", lead, D)
-    _check("mxfp4_quantize", ("x", x, _VALUES, x.shape), ("codes", codes, _U8, cs), ("bscale", bscale, _U8, bs))
+    dev = _check("mxfp4_quantize", ("x", x, _VALUES, x.shape), ("codes", codes, _U8, cs), ("bscale", bscale, _U8, bs))
     if codes is None:
         codes = _new("mxfp4_quantize", cs, torch.uint8, _U8, x.device)
     if bscale is None:
         bscale = _new("mxfp4_quantize", bs, torch.uint8, _U8, x.device)
     st = _lib.load().mxfp4_quantize(x.data_ptr(), _DT[x.dtype], x.numel() // D, D, codes.data_ptr(),
-                                    bscale.data_ptr(), _stream(stream))
+                                    bscale.data_ptr(), _stream(stream, dev))
     _lib.check("mxfp4_quantize", st)
     return codes, bscale
 
@@ -283,12 +284,12 @@ def mxfp4_dequantize(codes, bscale, out=None, *, dtype=torch.bfloat16, stream=No
     *lead, half = codes.shape
     D = 2 * half
     _, bs = _mxfp4_shapes("mxfp4_dequantize", lead, D)
-    _check("mxfp4_dequantize", ("codes", codes, _U8, codes.shape), ("bscale", bscale, _U8, bs),
+    dev = _check("mxfp4_dequantize", ("codes", codes, _U8, codes.shape), ("bscale", bscale, _U8, bs),
            ("out", out, _VALUES, (*lead, D)))
     if out is None:
         out = _new("mxfp4_dequantize", (*lead, D), dtype, _VALUES, codes.device)
     st = _lib.load().mxfp4_dequantize(codes.data_ptr(), bscale.data_ptr(), out.numel() // D, D, _DT[out.dtype],
-                                      out.data_ptr(), _stream(stream))
+                                      out.data_ptr(), _stream(stream, dev))
     _lib.check("mxfp4_dequantize", st)
     return out
 
@@ -297,13 +298,13 @@ def mxfp4_matmul(a_codes, a_bscale, b_codes, b_bscale, out=None, *, dtype=torch.
     """out [M, N] = a b^T of MXFP4 matrices (mxfp4_quantize): a_codes [M, K/2], a_bscale [M, K/32],
     b_codes [N, K/2], b_bscale [N, K/32]; out fp32 or bf16 (`dtype`, or out's)."""
     (M, half), (N, _) = a_codes.shape, b_codes.shape
-    _check("mxfp4_matmul", ("a_codes", a_codes, _U8, (M, half)), ("a_bscale", a_bscale, _U8, (M, half // 16)),
+    dev = _check("mxfp4_matmul", ("a_codes", a_codes, _U8, (M, half)), ("a_bscale", a_bscale, _U8, (M, half // 16)),
            ("b_codes", b_codes, _U8, (N, half)), ("b_bscale", b_bscale, _U8, (N, half // 16)),
            ("out", out, _VALUES, (M, N)), ("dev_status", dev_status, _I32, (1,)))
     if out is None:
         out = _new("mxfp4_matmul", (M, N), dtype, _VALUES, a_codes.device)
     st = _lib.load().mxfp4_matmul(a_codes.data_ptr(), a_bscale.data_ptr(), b_codes.data_ptr(), b_bscale.data_ptr(),
-                                  M, N, 2 * half, _DT[out.dtype], out.data_ptr(), _ptr(dev_status), _stream(stream))
+                                  M, N, 2 * half, _DT[out.dtype], out.data_ptr(), _ptr(dev_status), _stream(stream, dev))
     _lib.check("mxfp4_matmul", st)
     return out
 
@@ -316,12 +317,12 @@ def kv_quantize_fp4(rows, out=None, *, dst=None, dev_status=None, stream=None):
     if out is None and dst is not None:
         raise ValueError("kv_quantize_fp4: dst needs the cache it points into (out)")
     cap = out.shape[0] if out is not None else n
-    _check("kv_quantize_fp4", ("rows", rows, _VALUES, (n, 256)), ("out", out, _U8, (cap, KV4_ROW_BYTES)),
+    dev = _check("kv_quantize_fp4", ("rows", rows, _VALUES, (n, 256)), ("out", out, _U8, (cap, KV4_ROW_BYTES)),
            ("dst", dst, _I64, (n,)), ("dev_status", dev_status, _I32, (1,)))
     if out is None:
         out = _new("kv_quantize_fp4", (n, KV4_ROW_BYTES), torch.uint8, _U8, rows.device)
     st = _lib.load().kv_quantize_fp4(rows.data_ptr(), _DT[rows.dtype], n, _ptr(dst), cap, out.data_ptr(),
-                                     _ptr(dev_status), _stream(stream))
+                                     _ptr(dev_status), _stream(stream, dev))
     _lib.check("kv_quantize_fp4", st)
     return out
 
@@ -331,12 +332,12 @@ def kv_dequantize_fp4(cache, out=None, *, src=None, dtype=torch.bfloat16, dev_st
     src [n] int64 of it (negative: zeros), or its first rows (all of them without `out`)."""
     cap = cache.shape[0]
     n = src.shape[0] if src is not None else out.shape[0] if out is not None else cap
-    _check("kv_dequantize_fp4", ("cache", cache, _U8, (cap, KV4_ROW_BYTES)), ("out", out, _VALUES, (n, 256)),
+    dev = _check("kv_dequantize_fp4", ("cache", cache, _U8, (cap, KV4_ROW_BYTES)), ("out", out, _VALUES, (n, 256)),
            ("src", src, _I64, (n,)), ("dev_status", dev_status, _I32, (1,)))
     if out is None:
         out = _new("kv_dequantize_fp4", (n, 256), dtype, _VALUES, cache.device)
     st = _lib.load().kv_dequantize_fp4(cache.data_ptr(), _ptr(src), cap, n, _DT[out.dtype], out.data_ptr(),
-                                       _ptr(dev_status), _stream(stream))
+                                       _ptr(dev_status), _stream(stream, dev))
     _lib.check("kv_dequantize_fp4", st)
     return out
 

@@ -169,14 +169,6 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnParams p) 
   pdl_launch_dependents();  // the merge kernel waits for this grid before it reads
 }
 
-// Merge the splits of each query ([TR] §3.1), the sink once ([SW] §十二):
-//   M = max(max_s m_s, sink), L = sum_s 2^{m_s - M} l_s + 2^{sink - M},
-//   o = sum_s 2^{m_s - M} acc_s / L,   lse = ln 2 * (M + log2 L).
-// CTA (block of kCombineDims output dimensions, query); thread (head h, split group g), group g
-// taking splits g, g + kCombineGroups, ...  With few splits every load is issued at once and
-// each group folds its splits under its own max; otherwise two passes with independent loads
-// (so many are in flight at once): the max over the splits' m, merged across groups in shared
-// memory, then the weighted sums of l and acc under that common max, summed across groups.
 // Element i of the output, in its dtype.
 __device__ __forceinline__ void store_out(const AttnParams& p, size_t i, float v) {
   if (p.out_bf16)
@@ -185,6 +177,14 @@ __device__ __forceinline__ void store_out(const AttnParams& p, size_t i, float v
     p.out[i] = v;
 }
 
+// Merge the splits of each query ([TR] §3.1), the sink once ([SW] §十二):
+//   M = max(max_s m_s, sink), L = sum_s 2^{m_s - M} l_s + 2^{sink - M},
+//   o = sum_s 2^{m_s - M} acc_s / L,   lse = ln 2 * (M + log2 L).
+// CTA (block of kCombineDims output dimensions, query); thread (head h, split group g), group g
+// taking splits g, g + kCombineGroups, ...  With few splits every load is issued at once and
+// each group folds its splits under its own max; otherwise two passes with independent loads
+// (so many are in flight at once): the max over the splits' m, merged across groups in shared
+// memory, then the weighted sums of l and acc under that common max, summed across groups.
 constexpr int kCombineDims = 2;
 constexpr int kCombineGroups = 4;
 constexpr int kFewSplits = 5;  // splits per group folded in one round of loads

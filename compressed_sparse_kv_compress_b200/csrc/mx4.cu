@@ -7,8 +7,10 @@
 // NaN stays the largest), and a warp's loads and code stores are contiguous.
 // (Sixteen values a lane halve the shuffles, but the loads were no longer contiguous: slower.)
 // Measured, quantised and back: 262144 x 64 bf16, 85 MB in 15.0 us, 5.65 TB/s, 0.86 of the copy rate;
-// 262144 main-KV rows from bf16, 361 MB in 75 us, 4.8 TB/s, 0.73 (issue active 68 % of the cycles);
+// 262144 main-KV rows from bf16, 180 MB in 34.5 us, 5.2 TB/s, 0.80, and back in 30 us, 6.0 TB/s, 0.92;
 // a few rows: the latency of two launches, 2.1 us.
+#include <algorithm>
+
 #include "launch.cuh"
 #include "mx4.cuh"
 
@@ -19,22 +21,66 @@ constexpr int kMxUnroll = 4;                          // 256-value pieces of a w
 constexpr int kMxWarpValues = 256 * kMxUnroll;        // values a warp takes
 constexpr int kMxCtaValues = kMxWarpValues * (kMxThreads / 32);
 
-// Largest magnitude (as bits; an infinity or a NaN stays the largest) of the four lanes that hold a
-// block.
-__device__ __forceinline__ uint32_t block_amax(const float (&x)[8]) {
-  float a = fabsf(x[0]), b = fabsf(x[4]);
-#pragma unroll
-  for (int i = 1; i < 4; ++i) a = amax_nan(a, x[i]), b = amax_nan(b, x[4 + i]);
+// Eight neighbouring values as they are stored.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+};
+
+// Largest magnitude of the block that four lanes hold, as the bits of an fp32 value (an infinity or a NaN
+// stays the largest).  bf16: in pairs.
+__device__ __forceinline__ uint32_t amax_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t block_amax(const Raw8<__nv_bfloat16>& x) {
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  uint32_t m = amax_nan_bf16x2(amax_nan_bf16x2(x.w.x & kAbs, x.w.y & kAbs), amax_nan_bf16x2(x.w.z & kAbs, x.w.w & kAbs));
+  m = amax_nan_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = amax_nan_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  return max(m << 16, m & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint32_t block_amax(const Raw8<float>& x) {
+  const float a = amax_nan(amax_nan(amax_nan(fabsf(x.a.x), x.a.y), x.a.z), x.a.w);
+  const float b = amax_nan(amax_nan(amax_nan(fabsf(x.b.x), x.b.y), x.b.z), x.b.w);
   uint32_t m = __float_as_uint(amax_nan(a, b));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
 
 // x * 2^(127 - e) for the conversion.
-__device__ __forceinline__ void scale_down(float (&x)[8], uint32_t e) {
-  const float inv = mx_inv_scale(e);
+__device__ __forceinline__ void mul_pair(float a, float b, uint64_t s, float& x, float& y) {
+  uint64_t d;
+  asm("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tmul.rn.f32x2 %0, t, %3;\n\t}" : "=l"(d) : "f"(a), "f"(b), "l"(s));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(d));
+}
+__device__ __forceinline__ uint64_t twice(float s) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(s));
+  return d;
+}
+__device__ __forceinline__ void scaled_down(const Raw8<__nv_bfloat16>& r, uint32_t e, float (&x)[8]) {
+  const uint64_t s = twice(mx_inv_scale(e));
+  const uint32_t w[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] *= inv;
+  for (int i = 0; i < 4; ++i)
+    mul_pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u), s, x[2 * i], x[2 * i + 1]);
+}
+__device__ __forceinline__ void scaled_down(const Raw8<float>& r, uint32_t e, float (&x)[8]) {
+  const uint64_t s = twice(mx_inv_scale(e));
+  mul_pair(r.a.x, r.a.y, s, x[0], x[1]), mul_pair(r.a.z, r.a.w, s, x[2], x[3]);
+  mul_pair(r.b.x, r.b.y, s, x[4], x[5]), mul_pair(r.b.z, r.b.w, s, x[6], x[7]);
 }
 
 // Eight decoded values of a lane, stored: bf16 pairs straight from the codes, fp32 by value.
@@ -70,22 +116,18 @@ __global__ void __launch_bounds__(kMxThreads) mxfp4_quantize_kernel(const T* __r
   const T* from = x + b0 * kMxBlock + 8 * lane;
   uint8_t* to = codes + b0 * (kMxBlock / 2) + 4 * lane;
   const int left = (int)min((int64_t)(8 * kMxUnroll), blocks - b0) - (lane >> 2);  // blocks from this lane's first on
-  float f[kMxUnroll][8];
+  Raw8<T> r[kMxUnroll] = {};
 #pragma unroll
-  for (int u = 0; u < kMxUnroll; ++u) {
-    if (left > 8 * u)
-      Vec8<T>::load(from + 256 * u, f[u]);
-    else
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[u][i] = 0.f;
-  }
+  for (int u = 0; u < kMxUnroll; ++u)
+    if (left > 8 * u) r[u].load(from + 256 * u);
   uint32_t mine = 0;
 #pragma unroll
   for (int u = 0; u < kMxUnroll; ++u) {
-    const uint32_t e = mx_scale_code(block_amax(f[u]), kE2m1Emax);
-    scale_down(f[u], e);
+    const uint32_t e = mx_scale_code(block_amax(r[u]), kE2m1Emax);
+    float f[8];
+    scaled_down(r[u], e, f);
     if ((lane & 3) == u) mine = e;
-    if (left > 8 * u) *reinterpret_cast<uint32_t*>(to + 128 * u) = e == 0xFFu ? 0u : e2m1x8(f[u]);
+    if (left > 8 * u) *reinterpret_cast<uint32_t*>(to + 128 * u) = e == 0xFFu ? 0u : e2m1x8(f);
   }
   // lane l keeps the scale of piece l % 4, block l / 4: a warp's 32 scale bytes in one store
   const int64_t b = b0 + 8 * (lane & 3) + (lane >> 2);
@@ -117,12 +159,14 @@ __global__ void __launch_bounds__(kMxThreads) mxfp4_dequantize_kernel(const uint
 // A warp takes four rows as four groups of 32 lanes with eight values each: three groups are the
 // rows' 96 E2M1 pieces, one their 32 E4M3 pieces, so no lane waits for the other format's code
 // (with a row a warp both codes ran for every row, and the kernels were bound by issue: 41 and 44 us
-// for 262144 rows).
+// for 262144 rows; 37 and 37 with four rows a warp and no loop, whose address arithmetic was half of
+// the instructions).
 constexpr int kKv4Warps = 8;
 constexpr int kKv4Rows = 4;
+constexpr int64_t kKv4MostCtas = 16 * 148;  // a warp works out its pieces' places once, then strides over the rows
 
 // Piece of a lane in group j: the row among the warp's four, and where its eight values, its codes
-// and its block's scale sit in a row.
+// and its block's scale sit (from the first row's values, and from its bytes).
 struct Kv4Piece {
   int row, value, code, scale;
 };
@@ -142,86 +186,113 @@ __device__ __forceinline__ Kv4Piece kv4_piece(int j, int lane) {
   return p;
 }
 
-template <typename T>
+// LIST: rows go to the cache rows of a list (elsewhere: to their own numbers).  A warp puts its four
+// rows together in shared memory and stores them in 16-byte pieces, whole sectors of neighbouring rows
+// (4-byte codes and single scale bytes, stored from the lanes that hold them, took 37 us for 262144 rows, this 34).
+template <typename T, bool LIST>
 __global__ void __launch_bounds__(32 * kKv4Warps) kv_quantize_fp4_kernel(const T* __restrict__ rows, int64_t n,
                                                                         const int64_t* __restrict__ dst, int64_t cap,
                                                                         uint8_t* __restrict__ out, int* st) {
+  __shared__ uint4 made[kKv4Warps][kKv4Rows * kKv4RowBytes / 16];
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t r0 = ((int64_t)blockIdx.x * kKv4Warps + (threadIdx.x >> 5)) * kKv4Rows;
-  if (r0 >= n) return;
-  const int here = (int)min((int64_t)kKv4Rows, n - r0);  // rows of this warp
-  const T* from = rows + (size_t)r0 * kRow;
-  float x[4][8];
-  int64_t to[4];
+  uint4* mine = made[threadIdx.x >> 5];
+  uint8_t* bytes = reinterpret_cast<uint8_t*>(mine);
+  constexpr int kPieces = kKv4RowBytes / 16;  // 16-byte pieces of a row
+  Kv4Piece q[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const Kv4Piece q = kv4_piece(j, lane);
+  for (int j = 0; j < 4; ++j) q[j] = kv4_piece(j, lane);
+  if (lane < kKv4Rows) *reinterpret_cast<uint2*>(bytes + lane * kKv4RowBytes + kKv4Scales + 8) = make_uint2(0u, 0u);
+  const int64_t step = (int64_t)gridDim.x * kKv4Warps * kKv4Rows;
+  int64_t r0 = ((int64_t)blockIdx.x * kKv4Warps + (threadIdx.x >> 5)) * kKv4Rows;
+  Raw8<T> x[4];
+  auto load = [&](int64_t at, int j) {
     // past the end: the warp's first row again, not stored
-    const int row = q.row < here ? q.row : 0;
-    to[j] = dst ? __ldg(dst + r0 + row) : r0 + row;
-    Vec8<T>::load(from + (row * kRow + q.value), x[j]);
-    if (q.row >= here) to[j] = -1;
-  }
+    const int row = at + q[j].row < n ? q[j].row : 0;
+    x[j].load(rows + (size_t)at * kRow + (row * kRow + q[j].value));
+  };
+  if (r0 < n)
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const Kv4Piece q = kv4_piece(j, lane);
-    const uint32_t e = mx_scale_code(block_amax(x[j]), j == 3 ? kE4m3Emax : kE2m1Emax);
-    scale_down(x[j], e);
-    if (to[j] < 0) continue;
-    if (to[j] >= cap) {
-      if (q.value == 64) flag(st, CSKV_DEV_BAD_INDEX);  // once a row
-      continue;
+    for (int j = 0; j < 4; ++j) load(r0, j);
+  for (; r0 < n; r0 += step) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t e = mx_scale_code(block_amax(x[j]), j == 3 ? kE4m3Emax : kE2m1Emax);
+      float y[8];
+      scaled_down(x[j], e, y);
+      if (r0 + step < n) load(r0 + step, j);  // the next rows' values, behind this group's
+      uint8_t* o = bytes + q[j].row * kKv4RowBytes;
+      if (j == 3) {
+        const uint2 w = e4m3x8(y);
+        *reinterpret_cast<uint2*>(o + q[j].code) = e == 0xFFu ? make_uint2(0u, 0u) : w;
+      } else {
+        *reinterpret_cast<uint32_t*>(o + q[j].code) = e == 0xFFu ? 0u : e2m1x8(y);
+      }
+      if ((lane & 3) == 0) o[q[j].scale] = (uint8_t)e;
     }
-    uint8_t* o = out + (size_t)to[j] * kKv4RowBytes;
-    if (j == 3) {
-      const uint2 w = e4m3x8(x[j]);
-      *reinterpret_cast<uint2*>(o + q.code) = e == 0xFFu ? make_uint2(0u, 0u) : w;
-    } else {
-      *reinterpret_cast<uint32_t*>(o + q.code) = e == 0xFFu ? 0u : e2m1x8(x[j]);
+    __syncwarp();
+    const int pieces = (int)min((int64_t)kKv4Rows, n - r0) * kPieces;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int i = lane + 32 * u;
+      if (i >= pieces) continue;
+      if (LIST) {
+        const int row = i / kPieces;
+        const int64_t to = __ldg(dst + r0 + row);
+        if (to >= cap && i == row * kPieces) flag(st, CSKV_DEV_BAD_INDEX);
+        if (to >= 0 && to < cap) reinterpret_cast<uint4*>(out + (size_t)to * kKv4RowBytes)[i - row * kPieces] = mine[i];
+      } else {
+        reinterpret_cast<uint4*>(out + (size_t)r0 * kKv4RowBytes)[i] = mine[i];
+      }
     }
-    // a block's first lane stores its scale, its second one zero byte of the row's end
-    if ((lane & 3) < 2) o[q.scale + ((lane & 1) ? 8 : 0)] = (lane & 1) ? 0 : (uint8_t)e;
+    __syncwarp();
   }
 }
 
-template <typename T>
+template <typename T, bool LIST>
 __global__ void __launch_bounds__(32 * kKv4Warps) kv_dequantize_fp4_kernel(const uint8_t* __restrict__ cache,
                                                                           const int64_t* __restrict__ src,
                                                                           int64_t cap, int64_t n,
                                                                           T* __restrict__ out, int* st) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t r0 = ((int64_t)blockIdx.x * kKv4Warps + (threadIdx.x >> 5)) * kKv4Rows;
-  if (r0 >= n) return;
-  const int here = (int)min((int64_t)kKv4Rows, n - r0);  // rows of this warp
-  // all groups' loads go out before the first is decoded
-  uint2 w[4];
-  uint32_t e[4];
+  Kv4Piece q[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const Kv4Piece q = kv4_piece(j, lane);
-    int64_t i = q.row >= here ? -1 : src ? __ldg(src + r0 + q.row) : r0 + q.row;
-    if (i >= cap) {
-      if (q.value == 64) flag(st, CSKV_DEV_BAD_INDEX);  // once a row
-      i = -1;
+  for (int j = 0; j < 4; ++j) q[j] = kv4_piece(j, lane);
+  const int64_t step = (int64_t)gridDim.x * kKv4Warps * kKv4Rows;
+  for (int64_t r0 = ((int64_t)blockIdx.x * kKv4Warps + (threadIdx.x >> 5)) * kKv4Rows; r0 < n; r0 += step) {
+    const int here = (int)min((int64_t)kKv4Rows, n - r0);  // rows of this warp
+    const uint8_t* base = cache + (LIST ? 0 : (size_t)r0 * kKv4RowBytes);
+    // all groups' loads go out before the first is decoded
+    uint2 w[4];
+    uint32_t e[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w[j] = make_uint2(0u, 0u), e[j] = 127u;
+      if (q[j].row >= here) continue;
+      const uint8_t* row = base + q[j].row * kKv4RowBytes;
+      if (LIST) {
+        const int64_t i = __ldg(src + r0 + q[j].row);
+        if (i >= cap && q[j].value == 64) flag(st, CSKV_DEV_BAD_INDEX);  // once a row
+        if (i < 0 || i >= cap) continue;
+        row = base + (size_t)i * kKv4RowBytes;
+      }
+      if (j == 3)
+        w[j] = __ldg(reinterpret_cast<const uint2*>(row + q[j].code));
+      else
+        w[j].x = __ldg(reinterpret_cast<const uint32_t*>(row + q[j].code));
+      e[j] = __ldg(row + q[j].scale);
     }
-    const uint8_t* row = cache + (size_t)(i < 0 ? 0 : i) * kKv4RowBytes;
-    if (j == 3)
-      w[j] = i < 0 ? make_uint2(0u, 0u) : __ldg(reinterpret_cast<const uint2*>(row + q.code));
-    else
-      w[j] = make_uint2(i < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t*>(row + q.code)), 0u);
-    e[j] = i < 0 ? 127u : __ldg(row + q.scale);
-  }
+    T* to = out + (size_t)r0 * kRow;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const Kv4Piece q = kv4_piece(j, lane);
-    if (q.row >= here) continue;
-    T* to = out + (size_t)r0 * kRow + (q.row * kRow + q.value);
-    if (j == 3)
-      store_e4m3x8(to, w[j].x, w[j].y, e[j]);
-    else
-      store_e2m1x8(to, w[j].x, e[j]);
+    for (int j = 0; j < 4; ++j) {
+      if (q[j].row >= here) continue;
+      T* at = to + (q[j].row * kRow + q[j].value);
+      if (j == 3)
+        store_e4m3x8(at, w[j].x, w[j].y, e[j]);
+      else
+        store_e2m1x8(at, w[j].x, e[j]);
+    }
   }
 }
 
@@ -252,22 +323,34 @@ cudaError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales,
                          (__nv_bfloat16*)out);
 }
 
+static int64_t kv4_ctas(int64_t n) {
+  return std::min(kKv4MostCtas, (n + kKv4Warps * kKv4Rows - 1) / (kKv4Warps * kKv4Rows));
+}
+
+template <typename T>
+static cudaError_t launch_kv4_quantize_as(const void* rows, int64_t n, const int64_t* dst, int64_t cap, uint8_t* out,
+                                          int* st, cudaStream_t stream) {
+  return launch_1d(dst ? kv_quantize_fp4_kernel<T, true> : kv_quantize_fp4_kernel<T, false>, kv4_ctas(n),
+                   32 * kKv4Warps, stream, (const T*)rows, n, dst, cap, out, st);
+}
+
 cudaError_t launch_kv_quantize_fp4(const void* rows, int dtype, int64_t n, const int64_t* dst, int64_t cap,
                                    uint8_t* out, int* st, cudaStream_t stream) {
-  const int64_t ctas = (n + kKv4Warps * kKv4Rows - 1) / (kKv4Warps * kKv4Rows);
-  return dtype == CSKV_F32 ? launch_1d(kv_quantize_fp4_kernel<float>, ctas, 32 * kKv4Warps, stream, (const float*)rows,
-                                       n, dst, cap, out, st)
-                           : launch_1d(kv_quantize_fp4_kernel<__nv_bfloat16>, ctas, 32 * kKv4Warps, stream,
-                                       (const __nv_bfloat16*)rows, n, dst, cap, out, st);
+  return dtype == CSKV_F32 ? launch_kv4_quantize_as<float>(rows, n, dst, cap, out, st, stream)
+                           : launch_kv4_quantize_as<__nv_bfloat16>(rows, n, dst, cap, out, st, stream);
+}
+
+template <typename T>
+static cudaError_t launch_kv4_dequantize_as(const uint8_t* cache, const int64_t* src, int64_t cap, int64_t n,
+                                            void* out, int* st, cudaStream_t stream) {
+  return launch_1d(src ? kv_dequantize_fp4_kernel<T, true> : kv_dequantize_fp4_kernel<T, false>, kv4_ctas(n),
+                   32 * kKv4Warps, stream, cache, src, cap, n, (T*)out, st);
 }
 
 cudaError_t launch_kv_dequantize_fp4(const uint8_t* cache, const int64_t* src, int64_t cap, int64_t n, int dtype,
                                      void* out, int* st, cudaStream_t stream) {
-  const int64_t ctas = (n + kKv4Warps * kKv4Rows - 1) / (kKv4Warps * kKv4Rows);
-  return dtype == CSKV_F32 ? launch_1d(kv_dequantize_fp4_kernel<float>, ctas, 32 * kKv4Warps, stream, cache, src, cap,
-                                       n, (float*)out, st)
-                           : launch_1d(kv_dequantize_fp4_kernel<__nv_bfloat16>, ctas, 32 * kKv4Warps, stream, cache,
-                                       src, cap, n, (__nv_bfloat16*)out, st);
+  return dtype == CSKV_F32 ? launch_kv4_dequantize_as<float>(cache, src, cap, n, out, st, stream)
+                           : launch_kv4_dequantize_as<__nv_bfloat16>(cache, src, cap, n, out, st, stream);
 }
 
 }  // namespace cskv

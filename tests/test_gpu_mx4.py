@@ -190,3 +190,31 @@ def test_empty_calls_and_refusals():
         api.kv_quantize_fp4(rows, torch.zeros(3, 176, dtype=torch.uint8, device=d))  # fewer rows than n
     with pytest.raises(ValueError):
         api.kv_dequantize_fp4(torch.zeros(4, 176, dtype=torch.uint8, device=d), src=torch.zeros(2, device=d))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_rows_are_the_rows_of_small_calls(dtype):
+    # more rows than one pass of the grid takes (a ragged end too): the same bytes as calls of 1000
+    # rows, with and without lists, and back
+    n = 151_559
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(n, 256, device="cuda", generator=g).to(dtype)
+    x[n - 1, 7] = float("inf")
+    small = torch.cat([api.kv_quantize_fp4(x[i:i + 1000].contiguous()) for i in range(0, n, 1000)])
+    whole = api.kv_quantize_fp4(x)
+    assert torch.equal(whole, small)
+    perm = torch.randperm(n, device="cuda", generator=g)
+    dst = torch.where(perm % 7 == 3, torch.full_like(perm, -1), perm)
+    cache = torch.full((n, 176), 0xAB, dtype=torch.uint8, device="cuda")
+    api.kv_quantize_fp4(x, cache, dst=dst)
+    kept = dst >= 0
+    want = torch.full_like(cache, 0xAB)
+    want[dst[kept]] = small[kept]
+    assert torch.equal(cache, want)
+    back = api.kv_dequantize_fp4(whole, dtype=dtype)
+    parts = torch.cat([api.kv_dequantize_fp4(small[i:i + 1000].contiguous(), dtype=dtype) for i in range(0, n, 1000)])
+    bits = torch.int32 if dtype == torch.float32 else torch.int16
+    assert torch.equal(back.view(bits), parts.view(bits))
+    listed = api.kv_dequantize_fp4(whole, src=dst, dtype=dtype)
+    assert torch.equal(listed[kept].view(bits), parts[dst[kept]].view(bits))
+    assert torch.count_nonzero(listed[~kept]) == 0
