@@ -11,14 +11,14 @@
 // or, for a few rows of a, b: the tile is then as narrow as those rows, and few tiles are split over
 // the inner length inside a thread-block cluster, since one step is a chain of latencies.
 //
-// What bounds it: a step (256 deep) of a 128 x 192 tile is four products of about 95 cycles, its
-// 41 KB take 640 at the 64 bytes a cycle that an SM reads from L2, and issuing it takes about 650
-// (a wait 80, six scale copies 150-200, the products 100, the commit 230), so the tensor pipe is
-// active for 44 % of the cycles.  Steps that count here: scales copied a step before their products
+// What bounds it: a step (256 deep) of a 128 x 192 tile is four products of about 95 cycles, but its
+// 41 KB take 640 at the 64 bytes a cycle that an SM reads from L2, and 640 at shared memory's 128,
+// where they are written and read once each; the issuing warp takes about 650 a step.  The tensor pipe
+// is active for 44 % of the cycles.  Steps that count here: scales copied a step before their products
 // (4096^3: 50.5 -> 46.4 us), one wait and one commit a step (41.0), a row's scales loaded one
 // sector, four steps, at a time (38.2).
 // Measured (device time): 4096^3, bf16 out: 38 us, 3.6 PFLOP/s; 4096 x 512 x 4096: 10.3 us; one row
-// x 4096 x 4096: 5.5 us, 1.6 TB/s of codes; 67 x 1000 x 2080: 9.9 us.
+// x 4096 x 4096: 5.5 us, 1.6 TB/s of codes; 67 x 1000 x 2080: 10.6 us.
 #include <cuda.h>
 
 #include "launch.cuh"
