@@ -16,16 +16,17 @@
 // are split over the SMs.
 //   warp 19     resolves row lists into a table of row addresses, up to four chunks ahead
 //   warps 16-17 copy the stored rows to shared memory, up to two chunks ahead
-//   warps 8-15  decode them to bf16 in the 128-byte-swizzle layout, 16 rows a warp
+//   warps 8-15  decode them to bf16 in the 128-byte-swizzle layout, four for K, four for V (with up to
+//               64 heads, warps 2, 3 and 6-11: see there)
 //   warp 18     one thread issues S = Q K^T and O (+)= P V; Q and P are A operands in tensor
 //               memory, so only K and V are read from shared memory
 //   warps 0-7   softmax: TMEM lane h is head h; S -> P in place, O rescaled when the running
 //               maximum grows by more than 2^8 (any reference serves the online softmax), output
 // Two K and three V buffers (32 KB each) and two S / P buffers pipeline the chunks, across queries
 // too.  The roles' loops are kept short: unrolled ones missed the instruction cache.
-// Measured (device time): 4096 queries of 64 heads over 1152 rows 509 us (155 GFLOP, 304 TFLOP/s; issue
-// active 53 % of the cycles, tensor pipe 26 %: each warp's chain of waits and instructions); one
-// query of 128 heads over 1152 rows 13.9 us, over 8320 rows 17.1 us; 64 ragged queries 22.4 us.
+// Measured (device time): 4096 queries of 64 heads over 1152 rows 462 us (155 GFLOP, 335 TFLOP/s; the
+// softmax warps wait for 13 % of the time, the others longer: a warp's own chain of instructions); one
+// query of 128 heads over 1152 rows 13.9 us, over 8320 rows 17.0 us; 64 ragged queries 22.2 us.
 #include "attn_rows.cuh"
 #include "mx4.cuh"
 #include "roles.cuh"
@@ -119,6 +120,12 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
   const int64_t items = (int64_t)p.T * S;
 
   const int quads = (H + 31) / 32, soft = 2 * quads;  // TMEM lane groups with heads, softmax warps at work
+  // This warp's number among the decoding warps (0-3 K, 4-7 V).  A warp's scheduler is its number mod 4,
+  // and the softmax warps have to be on their TMEM lanes' schedulers: with up to 64 heads those are two,
+  // and three of four decoding warps go to the other two (4096 queries: 508 -> 479 us; all of them
+  // there 534).
+  int dec = warp < k4Copy ? warp - k4SoftWarps : -1;
+  if (quads <= 2) dec = warp == 8 || warp == 9 ? warp - 2 : (warp & 2) && warp < 12 ? (warp >> 2) * 2 + (warp & 1) : -1;
 
   // ---- set-up that reads no input overlaps the previous kernel (dependent launch)
   if (warp == k4Mma) {
@@ -327,16 +334,22 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
       }
       __syncwarp();
     }
-  } else if (warp >= k4SoftWarps) {
+  } else if (dec >= 0) {
     // ---------------------------------------------------------------- rows -> bf16 in shared memory
     // Warps 0-3 of the eight decode K, the others V, 32 rows each, a few rows at a time through
     // short loops.  E2M1: sixteen rows' K blocks (lane l: row l % 16, block l / 16) or eight rows'
     // V blocks (row l % 8, block l / 8); E4M3: eight rows' sixteen codes (row l % 8, piece l / 8).
     // Eight neighbouring lanes hold the same piece of eight rows: their swizzled stores meet all
     // banks once, and so do their loads of rows 176 bytes apart.
-    const int gw = (warp - k4SoftWarps) & 3, l8 = lane & 7, l16 = lane & 15, pv = lane >> 3, pk = lane >> 4;
-    const bool is_v = warp >= k4SoftWarps + 4;
+    const int gw = dec & 3, l8 = lane & 7, l16 = lane & 15, pv = lane >> 3, pk = lane >> 4;
+    const bool is_v = dec >= 4;
     const int row0 = gw * 32;
+    // a lane's E2M1 block of each step of e2m1_rows rows: one code for K and V, two blocks a turn, since
+    // the instruction cache is what counts (one code each 474 us, four blocks a turn 575)
+    const int e2m1_rows = is_v ? 8 : 16, lr = is_v ? l8 : l16;
+    const uint32_t e2m1_code = lr * kKv4RowBytes + (is_v ? kKv4V + 16 * pv : 16 * pk);
+    const uint32_t e2m1_scale = lr * kKv4RowBytes + kKv4Scales + (is_v ? 4 + pv : pk);
+    const uint32_t e2m1_to = k4_off(row0 + lr, 4 * (is_v ? pv : pk));
     const uint32_t base = smem_u32(buf), raw_base = base + k4OffRaw + row0 * kKv4RowBytes;
     uint32_t g = 0;
     bool ok = true;
@@ -354,17 +367,15 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
       const uint32_t dst = base + (is_v ? k4OffV + sv * k4Half : sk * k4Half);
       if (row0 < m.nc) {
         if (raw != 0xFFFFFFFFu) {
-          if (is_v) {
-            uint32_t at = src + l8 * kKv4RowBytes, to = dst + k4_off(row0 + l8, 4 * pv);
+          uint32_t code = src + e2m1_code, scale = src + e2m1_scale, put = dst + e2m1_to;
 #pragma unroll 1
-            for (int j = 0; j < 4; ++j, at += 8 * kKv4RowBytes, to += 8 * 128)
-              put_e2m1_block(at + kKv4V + 16 * pv, at + kKv4Scales + 4 + pv, to);
-          } else {
-            uint32_t at = src + l16 * kKv4RowBytes, to = dst + k4_off(row0 + l16, 4 * pk);
-#pragma unroll 1
-            for (int j = 0; j < 2; ++j, at += 16 * kKv4RowBytes, to += 16 * 128)
-              put_e2m1_block(at + 16 * pk, at + kKv4Scales + pk, to);
-            at = src + l8 * kKv4RowBytes, to = dst + k4_off(row0 + l8, 8 + 2 * pv);
+          for (int j = 0; j < 32; j += 2 * e2m1_rows) {  // two blocks a turn
+            put_e2m1_block(code, scale, put);
+            put_e2m1_block(code + e2m1_rows * kKv4RowBytes, scale + e2m1_rows * kKv4RowBytes, put + e2m1_rows * 128);
+            code += 2 * e2m1_rows * kKv4RowBytes, scale += 2 * e2m1_rows * kKv4RowBytes, put += 2 * e2m1_rows * 128;
+          }
+          if (!is_v) {
+            uint32_t at = src + l8 * kKv4RowBytes, to = dst + k4_off(row0 + l8, 8 + 2 * pv);
 #pragma unroll 1
             for (int j = 0; j < 4; ++j, at += 8 * kKv4RowBytes, to += 8 * 128)
               put_e4m3_half(at + kKv4Rope + 16 * pv, at + kKv4Scales + 2 + (pv >> 1), to);
@@ -382,7 +393,7 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
           cp_async_wait_all();
         }
       }
-      if (warp == k4SoftWarps && lane == 0) sh.meta[slot] = m;
+      if (dec == 0 && lane == 0) sh.meta[slot] = m;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -391,7 +402,7 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
         mbar_arrive(&sh.tab_empty[slot]);
       }
     }
-  } else {
+  } else if (warp < k4SoftWarps) {
     // ---------------------------------------------------------------- softmax and output
     // warps w and w + 4 share the TMEM lanes of heads 32w .. 32w + 31: each takes half of a
     // chunk's columns, of Q's and of O's dims, and they exchange row maxima and sums
