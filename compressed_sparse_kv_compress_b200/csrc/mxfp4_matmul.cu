@@ -374,9 +374,11 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
         float f[kStep];
 #pragma unroll
         for (int i = 0; i < kStep; ++i) f[i] = __uint_as_float(v[i]);
-        if (split == 1 && kStep == 32 && wide_out && q0 + c + 32 <= p.q_rows) {
+        if (split == 1 && kStep == 32 && p.p_is_a) {
           // out[p, q]: the warp's 32 x 32 values cross in shared memory, so that lanes store whole
-          // stretches of a row (64 or 128 bytes) instead of 16 bytes of 32 rows
+          // stretches of a row (64 or 128 bytes) instead of single values of 32 rows: 16 bytes a lane, or
+          // one value where rows are not whole 16-byte words or the columns end (1498 x 1069 x 64 by
+          // single values of 32 rows 26 us, this 7.9)
 #pragma unroll
           for (int i = 0; i < 32; i += 8) {
             float x[8];
@@ -385,13 +387,20 @@ __global__ void __launch_bounds__(kMmThreads, 1) mxfp4_matmul_kernel(const __gri
             Vec8<T>::store(reinterpret_cast<T*>(cross + lane * kMmOutPad) + i, x);
           }
           __syncwarp();
-          constexpr int kLanes = 2 * sizeof(T);  // lanes of a row: 16 bytes each
+          if (wide_out && q0 + c + 32 <= p.q_rows) {
+            constexpr int kLanes = 2 * sizeof(T);  // lanes of a row: 16 bytes each
 #pragma unroll
-          for (int i = 0; i < kLanes; ++i) {
-            const int r = i * (32 / kLanes) + lane / kLanes, at = lane % kLanes;
-            const uint4 w = *reinterpret_cast<const uint4*>(cross + r * kMmOutPad + 16 * at);
-            if (pr - lane + r < p.p_rows)
-              *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + (pr - lane + r) * p.ld + q0 + c + at * (16 / sizeof(T))) = w;
+            for (int i = 0; i < kLanes; ++i) {
+              const int r = i * (32 / kLanes) + lane / kLanes, at = lane % kLanes;
+              const uint4 w = *reinterpret_cast<const uint4*>(cross + r * kMmOutPad + 16 * at);
+              if (pr - lane + r < p.p_rows)
+                *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + (pr - lane + r) * p.ld + q0 + c + at * (16 / sizeof(T))) = w;
+            }
+          } else if (q0 + c + lane < p.q_rows) {
+            const int rows = (int)min((int64_t)32, p.p_rows - (pr - lane));
+            T* to = reinterpret_cast<T*>(p.out) + (pr - lane) * p.ld + q0 + c + lane;
+#pragma unroll 4
+            for (int r = 0; r < rows; ++r, to += p.ld) *to = reinterpret_cast<const T*>(cross + r * kMmOutPad)[lane];
           }
           __syncwarp();
         } else if (split == 1) {
