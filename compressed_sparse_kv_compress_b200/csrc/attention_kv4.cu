@@ -57,7 +57,11 @@ struct K4Chunk {
 struct K4Shared {
   uint64_t tab_full[k4Table], tab_empty[k4Table], k_full[k4KStages], k_empty[k4KStages], v_full[k4VStages];
   uint64_t raw_full[k4RawStages], raw_empty[k4RawStages];
-  uint64_t v_empty[k4VStages], s_full[2], p_full[2], max_full[4], sum_full[4], o_done, q_full, bail;
+  // o_done: a phase a chunk, whose P V is complete; o_last: a phase a (query, split), whose last P V is.
+  // Waits are by parity, so a role may wait for a phase only when it knows the one before to be
+  // complete.  S of a chunk is issued ahead of the P V of the chunk before, so a chunk's softmax knows
+  // of the P V two chunks back: enough to wait for the one before its own, not for its own.
+  uint64_t v_empty[k4VStages], s_full[2], p_full[2], max_full[4], sum_full[4], o_done, o_last, q_full, bail;
   uint32_t tmem;
   int abort;
   K4Chunk tab_meta[k4Table], meta[k4Table];
@@ -158,6 +162,7 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
       mbar_init(&sh.sum_full[i], 2);
     }
     mbar_init(&sh.o_done, 1);
+    mbar_init(&sh.o_last, 1);
     mbar_init(&sh.q_full, soft);
     mbar_init(&sh.bail, 1);
     sh.abort = 0;
@@ -322,6 +327,7 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
                 tc_mma_f16_ta(tmem + k4ColO, tP + (kk >> 2) * 64 + (kk & 3) * 8, d + kk * 128, idesc_o, !first || kk > 0);
             tc_commit(&sh.v_empty[st]);
             tc_commit(&sh.o_done);
+            if (!more) tc_commit(&sh.o_last);
           }
           __syncwarp();
           if (nc) first = false;
@@ -529,7 +535,7 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
       sh.half_sum[half][h] = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.sum_full[quad]);
-      ok = k4_wait_warp(sh, &sh.sum_full[quad], n, p.st) && k4_wait_warp(sh, &sh.o_done, g - 1, p.st);
+      ok = k4_wait_warp(sh, &sh.sum_full[quad], n, p.st) && k4_wait_warp(sh, &sh.o_last, n, p.st);
       if (!ok) break;
       tc_fence_after();
       l += sh.half_sum[half ^ 1][h];
