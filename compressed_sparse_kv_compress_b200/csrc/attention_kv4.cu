@@ -65,7 +65,10 @@ struct K4Shared {
   uint32_t tmem;
   int abort;
   K4Chunk tab_meta[k4Table], meta[k4Table];
-  float half_max[2][2][128], half_sum[2][128];  // [chunk parity][column half][head], [half][head]
+  // [chunk parity][column half][head], [parity of the (query, split)][half][head]: the two warps of a
+  // group meet once a chunk with rows, and once a (query, split), so one of them may be a chunk or a
+  // (query, split) ahead of the other's reads
+  float half_max[2][2][128], half_sum[2][2][128];
   uint64_t row[k4Table][k4Chunk];               // address of each row; 0: skipped
 };
 
@@ -532,13 +535,13 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
       if (!ok) break;
       // every S of this query is complete: the next query's Q may take its place
       if (item + gridDim.x < items) put_q(item + gridDim.x);
-      sh.half_sum[half][h] = l;
+      sh.half_sum[n & 1][half][h] = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.sum_full[quad]);
       ok = k4_wait_warp(sh, &sh.sum_full[quad], n, p.st) && k4_wait_warp(sh, &sh.o_last, n, p.st);
       if (!ok) break;
       tc_fence_after();
-      l += sh.half_sum[half ^ 1][h];
+      l += sh.half_sum[n & 1][half ^ 1][h];
       const int t = (int)(item / S), split = (int)(item % S);
       const uint32_t tO = tmem + k4ColO + lane_base + 64 * half;
       if (S == 1) {

@@ -10,7 +10,7 @@ import torch
 
 from oracle import kv4
 
-from compressed_sparse_kv_compress_b200 import api
+from compressed_sparse_kv_compress_b200 import _lib, api
 from test_gpu_attn_kv4 import Case
 
 pytestmark = pytest.mark.gpu
@@ -82,3 +82,28 @@ def test_a_whole_prefill_chunk():
         assert bool(((out[t].double() - ref).abs() <= tol).all()), t0
         tl = dl + (R + 8) * 2.0 ** -23 + 2.0 ** -22 * (1 + rl.abs())
         assert bool(((lse[t].double() - rl).abs() <= tl).all()), t0
+
+
+@pytest.mark.parametrize("H", [16, 64, 128])
+@pytest.mark.parametrize("sink", [False, True])
+def test_empty_queries_between_others(H, sink):
+    """Dense mode without a window: a CTA's queries (every SMs-th of the list) have rows and none in turn,
+    some of them because their sequence does not exist."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    T = 6 * sms + 5
+    full = (np.arange(T) // sms) % 2 == 0
+    c = Case(api.HCA, [int(n) for n in np.where(full, 128 * (1 + np.arange(T) % 5) + 3, 1 + np.arange(T) % 127)],
+             [1] * T, H, W=0, sink=sink, seed=H)
+    d = c.dev()
+    ref = [c.run(torch.float32, d) for _ in range(8)]
+    c.check(ref[0][0], ref[0][1])
+    assert all(int(st.item()) == 0 for _, _, st in ref)
+    assert all(torch.equal(ref[0][0], o) and torch.equal(ref[0][1], e) for o, e, _ in ref)
+    none = np.flatnonzero(~full)
+    assert not ref[0][0][none].any()
+    d["q_seq"][none[::3]] = T
+    out, lse, st = c.run(torch.float32, d)
+    assert int(st.item()) == _lib.DEV_BAD_INDEX
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[none[::3]] = False
+    assert torch.equal(out, ref[0][0]) and torch.equal(lse[keep], ref[0][1][keep])
