@@ -542,6 +542,9 @@ __global__ void __launch_bounds__(k4Threads, 1) attn_kv4_kernel(const __grid_con
       if (!ok) break;
       tc_fence_after();
       l += sh.half_sum[n & 1][half ^ 1][h];
+      // maxima pass over NaN, sums do not: logits that are all NaN (or NaN and masked) leave l = NaN under
+      // m = -inf, which below and in the merge stands for no rows; any finite reference keeps them
+      if (l != l && m == -INFINITY) m = 0.f;
       const int t = (int)(item / S), split = (int)(item % S);
       const uint32_t tO = tmem + k4ColO + lane_base + 64 * half;
       if (S == 1) {
