@@ -121,9 +121,16 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnParams p) 
     // ---- online softmax per head
     for (int h = tid; h < H; h += kAttnThreads) {
       float mt = -INFINITY;
-      for (int rr = 0; rr < kAttnTile; ++rr) mt = fmaxf(mt, ps[h * kPsStride + rr]);
+      bool nan = false;
+      for (int rr = 0; rr < kAttnTile; ++rr) {
+        const float s = ps[h * kPsStride + rr];
+        nan |= s != s;
+        mt = fmaxf(mt, s);
+      }
       const float m_old = m_run[h];
-      const float m_new = fmaxf(m_old, mt);
+      // maxima pass over NaN, sums do not: under m = -inf, which stands for no rows, a NaN would be
+      // left out, so a tile with one takes a finite reference
+      const float m_new = nan && fmaxf(m_old, mt) == -INFINITY ? 0.f : fmaxf(m_old, mt);
       float al = 1.f, sum = 0.f;
       if (m_new != -INFINITY) {
         al = exp2f(m_old - m_new);
@@ -255,11 +262,11 @@ __global__ void __launch_bounds__(128 * kCombineGroups) attn_combine_kernel(Attn
         for (int jj = 0; jj < kCombineDims; ++jj) ot[jj] = fmaf(sO[gg][jj][h], f, ot[jj]);
       }
     }
-    const float inv = Lt > 0.f ? 1.f / Lt : 0.f;
+    const float inv = Lt > 0.f || Lt != Lt ? 1.f / Lt : 0.f;  // a NaN denominator stays one
     const size_t dst = ((size_t)t * H + h) * kHeadDim + j0;
 #pragma unroll
     for (int jj = 0; jj < kCombineDims; ++jj) store_out(p, dst + jj, ot[jj] * inv);
-    if (j0 == 0 && p.lse) p.lse[(size_t)t * H + h] = Lt > 0.f ? (Mt + log2f(Lt)) * 0.69314718055994531f : -INFINITY;
+    if (j0 == 0 && p.lse) p.lse[(size_t)t * H + h] = Lt > 0.f || Lt != Lt ? (Mt + log2f(Lt)) * 0.69314718055994531f : -INFINITY;
     return;
   }
   // ---- pass 1: M = max over all splits of m (log2 units)
@@ -311,11 +318,11 @@ __global__ void __launch_bounds__(128 * kCombineGroups) attn_combine_kernel(Attn
     fp = M == -INFINITY ? 0.f : exp2f(M - Mt);
     Lt = Ls * fp + (p.sink ? exp2f(sk - Mt) : 0.f);
   }
-  const float inv = Lt > 0.f ? fp / Lt : 0.f;
+  const float inv = Lt > 0.f || Lt != Lt ? fp / Lt : 0.f;
   const size_t dst = ((size_t)t * H + h) * kHeadDim + j0;
 #pragma unroll
   for (int jj = 0; jj < kCombineDims; ++jj) store_out(p, dst + jj, os[jj] * inv);
-  if (j0 == 0 && p.lse) p.lse[(size_t)t * H + h] = Lt > 0.f ? (Mt + log2f(Lt)) * 0.69314718055994531f : -INFINITY;
+  if (j0 == 0 && p.lse) p.lse[(size_t)t * H + h] = Lt > 0.f || Lt != Lt ? (Mt + log2f(Lt)) * 0.69314718055994531f : -INFINITY;
 }
 
 cudaError_t launch_attn_combine(const AttnParams& p, cudaStream_t stream) {

@@ -17,7 +17,7 @@ def _all_nan(out, lse, t):
     assert bool(out[t].isnan().all()) and bool(lse[t].isnan().all())
 
 
-@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("sink", [False, True])
 @pytest.mark.parametrize("T", [3, 200])
 def test_the_only_attended_row_is_nan(T, sink, dtype):
@@ -32,7 +32,7 @@ def test_the_only_attended_row_is_nan(T, sink, dtype):
     c.check(out, lse, skip_queries=(1,))
 
 
-@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_nan_in_a_split_of_its_own(dtype):
     """1024 selected rows and a window of one token, whose K is NaN: the last split holds that row alone."""
     c = Case(api.CSA, [9000], [1], 64, k=1024, W=1, dtype=dtype, seed=4)
@@ -41,7 +41,7 @@ def test_nan_in_a_split_of_its_own(dtype):
     _all_nan(out, lse, 0)
 
 
-@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T", [1, 160])
 def test_nan_rows_before_others(T, dtype):
     """The first 200 rows NaN, the rest numbers; and one NaN row behind 600 numbers."""
@@ -59,7 +59,7 @@ def test_nan_rows_before_others(T, dtype):
         _all_nan(out, lse, t)
 
 
-@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_a_nan_value_block_shows_in_its_dims_alone(dtype):
     """V dims 32..63 of one attended row: those dims NaN, the others and lse as without it."""
     c = Case(api.CSA, [4000], [2], 64, k=64, dtype=dtype, seed=6)
