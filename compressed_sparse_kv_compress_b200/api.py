@@ -206,7 +206,8 @@ def hybrid_decode_attn(mode, q, kv_cmp, cmp_off, kv_raw, raw_off, q_seq, q_pos, 
     positions; see the C header).  kv_fp8: CSKV_ATTN_KV_FP8, kv_cmp holds FP8 main-KV rows
     ([entries, 336] uint8, from kv_quantize_fp8).  kv_fp4: CSKV_ATTN_KV_FP4, kv_cmp holds 4-bit
     main-KV rows ([entries, 176] uint8, from kv_quantize_fp4).  out is [T, H, 128] fp32, or bf16
-    (CSKV_ATTN_OUT_BF16)."""
+    (CSKV_ATTN_OUT_BF16).  workspace: attn_workspace(...); bf16 queries over 4-bit rows may go without
+    (None) when they are more than half of the device's SMs."""
     T, H, d = q.shape
     if adjacent_pairs:
         mode = int(mode) | ATTN_PAIRS
@@ -221,12 +222,12 @@ def hybrid_decode_attn(mode, q, kv_cmp, cmp_off, kv_raw, raw_off, q_seq, q_pos, 
         mode = int(mode) | ATTN_OUT_BF16
     k = idx.shape[1] if idx is not None else 0
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     lib = _lib.load()
     st = lib.hybrid_decode_attn(int(mode), _ptr(q), _ptr(kv_cmp), _ptr(cmp_off), _ptr(idx), k, _ptr(kv_raw),
                                 _ptr(raw_off), _ptr(raw_tok0), int(window), _ptr(sink), scale, _ptr(q_seq),
                                 _ptr(q_pos), cmp_off.numel() - 1, T, H, d, _dt(q), int(max_entries), _ptr(out),
-                                _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                _ptr(dev_status), _stream(stream))
+                                _ptr(lse), _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(stream))
     _lib.check("hybrid_decode_attn", st)
     return out
 

@@ -552,7 +552,7 @@ int hybrid_decode_attn(int mode, const void* q, const void* kv_cmp, const int64_
     if (rc) return rc;
     pl.cluster = 0;
     attn_kv4_plan(T, (mode == CSKV_CSA ? (int64_t)k : max_entries) + window, sms, &pl.R, &pl.S);
-    pl.ws_splits = pl.S;
+    pl.ws_splits = pl.S > 1 ? pl.S : 0;  // one split writes its output itself
   }
   // adjacent-query pairs: the HCA tensor-core kernel with 64 heads, when the pairs' plan merges
   // inside a cluster (a unit of two queries is one 128-head "query" of the plan)
@@ -568,7 +568,7 @@ int hybrid_decode_attn(int mode, const void* q, const void* kv_cmp, const int64_
     }
   }
   const size_t need = (size_t)units * pl.ws_splits * Hv * (kHeadDim + 2) * sizeof(float);
-  if (!workspace || ws_bytes < need || !aligned16(workspace)) return CSKV_ERR_WORKSPACE;
+  if (need > 0 && (!workspace || ws_bytes < need || !aligned16(workspace))) return CSKV_ERR_WORKSPACE;
   AttnParams p = {};
   p.mode = mode;
   p.q = q;
@@ -595,8 +595,10 @@ int hybrid_decode_attn(int mode, const void* q, const void* kv_cmp, const int64_
   p.kv8 = kv8 ? 1 : 0;
   p.kv4 = kv4 ? 1 : 0;
   p.out_bf16 = out_bf16 ? 1 : 0;
-  p.part_acc = (float*)workspace;
-  p.part_ml = p.part_acc + (size_t)units * pl.S * Hv * kHeadDim;
+  if (need > 0) {
+    p.part_acc = (float*)workspace;
+    p.part_ml = p.part_acc + (size_t)units * pl.S * Hv * kHeadDim;
+  }
   p.out = out;
   p.lse = lse;
   p.st = dev_status;

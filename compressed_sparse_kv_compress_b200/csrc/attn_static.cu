@@ -8,7 +8,8 @@
 //
 // Limits and behaviour:
 //  * the array holds CSKV_NOALLOC_SCRATCH_BYTES; a call that needs more returns
-//    CSKV_ERR_WORKSPACE and launches nothing;
+//    CSKV_ERR_WORKSPACE and launches nothing (bf16 queries over 4-bit rows never do: their kernel
+//    splits queries over the SMs, so its partials are at most an SM's worth of heads each);
 //  * every GPU that loads this library keeps the array until the process exits;
 //  * all calls share the array and it keeps the last call's partials; the partials are
 //    always written before they are read, so nothing needs clearing, but two calls that
@@ -66,9 +67,13 @@ extern "C" int hybrid_decode_attn_noalloc(int mode, const void* q, const void* k
   const int arc = cskv::check_attn_args(mode, q, kv_cmp, cmp_off, idx, k, kv_raw, raw_off, window, scale, q_seq,
                                         q_pos, batch, T, H, d, dtype, max_entries, out);
   if (arc != CSKV_OK || T == 0) return arc;
-  const size_t need = hybrid_attn_workspace_size(mode, T, H, d, (mode & ~cskv::kAttnFlags) == CSKV_CSA ? k : 0,
-                                                 window, max_entries);
-  if (need > CSKV_NOALLOC_SCRATCH_BYTES) return CSKV_ERR_WORKSPACE;
+  // hybrid_attn_workspace_size covers every type's kernel; bf16 queries over 4-bit rows need what their own
+  // plan says, which the call below holds against the array
+  if (!((mode & CSKV_ATTN_KV_FP4) && dtype == CSKV_BF16)) {
+    const size_t need = hybrid_attn_workspace_size(mode, T, H, d, (mode & ~cskv::kAttnFlags) == CSKV_CSA ? k : 0,
+                                                   window, max_entries);
+    if (need > CSKV_NOALLOC_SCRATCH_BYTES) return CSKV_ERR_WORKSPACE;
+  }
   float* scratch = nullptr;
   const int rc = scratch_for_current_device(&scratch);
   if (rc != CSKV_OK) return rc;

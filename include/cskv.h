@@ -435,8 +435,10 @@ CSKV_API size_t lindex_workspace_size_scan(int T, int64_t max_entries);
  * mode | CSKV_ATTN_KV_FP4 : kv_cmp holds 4-bit main-KV rows (kv_quantize_fp4: 176 bytes a row,
  *           indexed by cmp_off like the plain rows); kv_raw stays in dtype.  bf16 queries run on
  *           the tensor cores over the rows decoded to bf16 (exact), fp32 ones on the CUDA cores;
- *           CSKV_ATTN_PAIRS is ignored.  The workspace size is the same.  Not together with
- *           CSKV_ATTN_KV_FP8.  out must be 16-byte aligned.
+ *           CSKV_ATTN_PAIRS is ignored.  The workspace size is the same and covers both types;
+ *           bf16 queries need less: [T, splits, H, d + 2] fp32 where a query's rows are split, T times
+ *           splits at most the device's SMs, and none with T above half of the SMs (workspace may
+ *           be NULL then).  Not together with CSKV_ATTN_KV_FP8.  out must be 16-byte aligned.
  * mode | CSKV_ATTN_OUT_BF16 : out is [T, H, d] bf16 (16-byte aligned), rounded to nearest even
  *           from the fp32 result; lse stays fp32.
  * ------------------------------------------------------------------------ */
@@ -460,7 +462,8 @@ CSKV_API size_t hybrid_attn_workspace_size(int mode, int T, int H, int d, int k,
  * in one array of CSKV_NOALLOC_SCRATCH_BYTES that the library declares in device memory.
  * After its first call on a device (below) it allocates nothing.
  * - A call whose hybrid_attn_workspace_size() exceeds CSKV_NOALLOC_SCRATCH_BYTES returns
- *   CSKV_ERR_WORKSPACE and launches nothing.
+ *   CSKV_ERR_WORKSPACE and launches nothing.  bf16 queries over 4-bit rows (CSKV_ATTN_KV_FP4) need
+ *   less than that size and always fit.
  * - Every GPU that loads the library holds the array until the process exits.
  * - All calls share the array, which keeps the last call's contents.  Nothing in it needs
  *   clearing (every partial is written before it is read), but calls that overlap on the

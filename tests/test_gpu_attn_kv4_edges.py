@@ -1,11 +1,11 @@
 """hybrid_decode_attn over 4-bit rows at its edges: NaN entries that are attended (a block with an infinity
-or a NaN reads as NaN, so it has to show in whatever attends to it)."""
+or a NaN reads as NaN, so it has to show in whatever attends to it), and calls that need no workspace."""
 
 import numpy as np
 import pytest
 import torch
 
-from compressed_sparse_kv_compress_b200 import api
+from compressed_sparse_kv_compress_b200 import CskvError, _lib, api
 from test_gpu_attn_kv4 import Case
 
 pytestmark = pytest.mark.gpu
@@ -71,3 +71,40 @@ def test_a_nan_value_block_shows_in_its_dims_alone(dtype):
     assert bool(out[1, :, 32:64].isnan().all())
     assert torch.equal(out[1, :, :32], ref[1, :, :32]) and torch.equal(out[1, :, 64:], ref[1, :, 64:])
     assert torch.equal(lse[1], ref_lse[1]) and bool(out[0].isfinite().all())
+
+
+@pytest.mark.parametrize("mode,k", [(api.CSA, 1024), (api.HCA, 0)])
+@pytest.mark.parametrize("T", [1, 70, 80, 400])
+def test_many_queries_without_a_workspace(mode, k, T):
+    """Queries that are not split write their outputs themselves: no workspace, and the allocation-free
+    variant takes any number of them.  Split queries: refused without one, and the variant's own fits."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    c = Case(mode, [200000], [T], 128, k=k, seed=7)
+    d = c.dev()
+    out, lse, _ = c.run(torch.bfloat16, d)
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+    lib = _lib.load()
+
+    def call(fn, *ws):
+        return fn(mode | _lib.ATTN_KV_FP4 | _lib.ATTN_OUT_BF16, p(d["q"]), p(d["cache"]), p(d["off"]), p(d["idx"]), k,
+                  p(d["raw"]), p(d["raw_off"]), p(d["t0"]), c.W, p(d["sink"]), 128 ** -0.5, p(d["q_seq"]), p(d["q_pos"]),
+                  1, T, 128, 128, _lib.BF16, c.most, p(o2), p(l2), *ws, None, torch.cuda.current_stream().cuda_stream)
+
+    assert call(lib.hybrid_decode_attn_noalloc) == _lib.OK
+    torch.cuda.synchronize()
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+    assert call(lib.hybrid_decode_attn, None, 0) == (_lib.OK if 2 * T > sms else _lib.ERR_WORKSPACE)
+
+    def without():
+        o2.fill_(7.0), l2.fill_(7.0)
+        api.hybrid_decode_attn(mode, d["q"], d["cache"], d["off"], d["raw"], d["raw_off"], d["q_seq"], d["q_pos"], o2, None,
+                               window=c.W, idx=d["idx"], raw_tok0=d["t0"], sink=d["sink"], lse=l2, max_entries=c.most,
+                               kv_fp4=True)
+
+    if 2 * T > sms:
+        without()
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+    else:
+        with pytest.raises(CskvError):
+            without()
