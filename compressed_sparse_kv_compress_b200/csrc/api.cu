@@ -197,10 +197,10 @@ static int check_value_dtype(int dtype) {
   return dtype == CSKV_FP8E4M3 ? CSKV_ERR_UNSUPPORTED : CSKV_ERR_INVALID_ARG;
 }
 
-// Shape and pointers of mxfp4_quantize / mxfp4_dequantize; 2^44 values bound the grid.
+// Shape and pointers of mxfp4_quantize / mxfp4_dequantize.
 static int check_mxfp4(const void* x, int dtype, int64_t rows, int64_t D, const uint8_t* codes,
                        const uint8_t* bscale) {
-  if (rows < 0 || D < 1 || D % 32 || D > (1LL << 44) || rows > (1LL << 44) / D) return CSKV_ERR_INVALID_ARG;
+  if (rows < 0 || D < 1 || D % 32 || D > kMxMostValues || rows > kMxMostValues / D) return CSKV_ERR_INVALID_ARG;
   const int rc = check_value_dtype(dtype);
   if (rc || rows == 0) return rc;
   if (!x || !codes || !bscale || !aligned16(x) || !aligned16(codes)) return CSKV_ERR_INVALID_ARG;

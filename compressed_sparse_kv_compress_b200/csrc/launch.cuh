@@ -168,6 +168,8 @@ int check_attn_args(int mode, const void* q, const void* kv_cmp, const int64_t* 
 // kv8.cu
 cudaError_t launch_kv_quantize_fp8(const void* rows, int dtype, int64_t n, uint8_t* out, cudaStream_t stream);
 // mx4.cu
+constexpr int kMxCtaValues = 8192;                                   // values that a CTA quantises
+constexpr int64_t kMxMostValues = ((1LL << 31) - 1) * kMxCtaValues;  // by the grid's 2^31 - 1 CTAs
 cudaError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t blocks, uint8_t* codes, uint8_t* scales,
                                   cudaStream_t stream);
 cudaError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t blocks, int dtype, void* out,

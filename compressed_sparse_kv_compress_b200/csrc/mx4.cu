@@ -19,7 +19,7 @@ namespace cskv {
 constexpr int kMxThreads = 256;
 constexpr int kMxUnroll = 4;                          // 256-value pieces of a warp in flight
 constexpr int kMxWarpValues = 256 * kMxUnroll;        // values a warp takes
-constexpr int kMxCtaValues = kMxWarpValues * (kMxThreads / 32);
+static_assert(kMxCtaValues == kMxWarpValues * (kMxThreads / 32));
 
 // Eight neighbouring values as they are stored.
 template <typename T>

@@ -195,7 +195,8 @@ CSKV_API int kv_quantize_fp8(const void* rows, int dtype, int64_t n, void* out, 
  * D        : a positive multiple of 32.
  * mxfp4_dequantize writes code x scale, rounded to dtype (exact but for bf16's range).
  * rows == 0 launches nothing.  Errors: CSKV_ERR_INVALID_ARG (null or misaligned pointer with
- * rows > 0, rows < 0, bad D or dtype, more than 2^44 values), CSKV_ERR_UNSUPPORTED (FP8).
+ * rows > 0, rows < 0, bad D or dtype, more than 2^44 - 8192 values), CSKV_ERR_UNSUPPORTED
+ * (FP8).
  * ------------------------------------------------------------------------ */
 CSKV_API int mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t D, uint8_t* codes, uint8_t* bscale,
                  cskv_stream_t stream);
