@@ -56,6 +56,7 @@ def _check(fn: str, *specs) -> int:
 _U8 = (torch.uint8,)
 _I64 = (torch.int64,)
 _I32 = (torch.int32,)
+_F32 = (torch.float32,)
 _VALUES = (torch.float32, torch.bfloat16)
 
 
@@ -199,6 +200,39 @@ def attn_workspace(mode, T, H, k, window, max_entries, device="cuda") -> torch.T
     return torch.empty(max(16, n), dtype=torch.uint8, device=device)
 
 
+def _check_attn_kv4(T, H, d, q, kv_cmp, cmp_off, kv_raw, raw_off, q_seq, q_pos, out, idx, raw_tok0, sink, lse, workspace,
+                    dev_status):
+    """Refuses what attention over 4-bit rows cannot take: its kernels read every array by the counts and
+    types that the C header gives.  A call's time for few queries is the host's, so what fits is seen
+    by elements and types first (that all are contiguous, as their pointers are taken); only what does
+    not goes through the check that names it."""
+    dev, B = torch.cuda.current_device(), cmp_off.numel() - 1
+    i64, i32, f32 = torch.int64, torch.int32, torch.float32
+    if (q.dtype in _VALUES and out.dtype in _VALUES and kv_raw.dtype is q.dtype and kv_cmp.dtype is torch.uint8
+            and out.shape == q.shape and kv_cmp.dim() == 2 and kv_cmp.shape[1] == KV4_ROW_BYTES
+            and kv_raw.dim() == 2 and kv_raw.shape[1] == 256
+            and cmp_off.dtype is i64 and raw_off.dtype is i64 and q_pos.dtype is i64 and q_seq.dtype is i32
+            and raw_off.numel() == B + 1 and q_pos.numel() == T and q_seq.numel() == T
+            and q.get_device() == dev and out.get_device() == dev and kv_raw.get_device() == dev
+            and kv_cmp.get_device() == dev and cmp_off.get_device() == dev and raw_off.get_device() == dev
+            and q_pos.get_device() == dev and q_seq.get_device() == dev
+            and (idx is None or idx.dtype is i32 and idx.dim() == 2 and idx.shape[0] == T and idx.get_device() == dev)
+            and (raw_tok0 is None or raw_tok0.dtype is i64 and raw_tok0.numel() == B and raw_tok0.get_device() == dev)
+            and (sink is None or sink.dtype is f32 and sink.numel() == H and sink.get_device() == dev)
+            and (lse is None or lse.dtype is f32 and lse.numel() == T * H and lse.get_device() == dev)
+            and (workspace is None or workspace.get_device() == dev)
+            and (dev_status is None or dev_status.dtype is i32 and dev_status.get_device() == dev)):
+        return
+    any_of = lambda t: ((t.dtype,), t.shape) if t is not None else (None, None)  # noqa: E731
+    _check("hybrid_decode_attn", ("q", q, _VALUES, (T, H, d)), ("kv_cmp", kv_cmp, _U8, (kv_cmp.shape[0], KV4_ROW_BYTES)),
+           ("kv_raw", kv_raw, (q.dtype,), (kv_raw.shape[0], 256)), ("out", out, _VALUES, (T, H, d)),
+           ("cmp_off", cmp_off, _I64, (B + 1,)), ("raw_off", raw_off, _I64, (B + 1,)), ("q_seq", q_seq, _I32, (T,)),
+           ("q_pos", q_pos, _I64, (T,)), ("idx", idx, _I32, (T, idx.shape[-1]) if idx is not None else None),
+           ("raw_tok0", raw_tok0, _I64, (B,)), ("sink", sink, _F32, (H,)), ("lse", lse, _F32, (T, H)),
+           ("dev_status", dev_status, _I32, dev_status.shape if dev_status is not None else None),
+           ("workspace", workspace, *any_of(workspace)))
+
+
 def hybrid_decode_attn(mode, q, kv_cmp, cmp_off, kv_raw, raw_off, q_seq, q_pos, out, workspace, *, window,
                        idx=None, raw_tok0=None, sink=None, scale=None, lse=None, max_entries=0, adjacent_pairs=False,
                        kv_fp8=False, kv_fp4=False, dev_status=None, stream=None):
@@ -215,9 +249,8 @@ def hybrid_decode_attn(mode, q, kv_cmp, cmp_off, kv_raw, raw_off, q_seq, q_pos, 
         mode = int(mode) | ATTN_KV_FP8
     if kv_fp4:
         mode = int(mode) | ATTN_KV_FP4
-        _check("hybrid_decode_attn", ("q", q, _VALUES, (T, H, d)),
-               ("kv_cmp", kv_cmp, _U8, (kv_cmp.shape[0], KV4_ROW_BYTES)),
-               ("kv_raw", kv_raw, (q.dtype,), (kv_raw.shape[0], 256)), ("out", out, _VALUES, (T, H, d)))
+        _check_attn_kv4(T, H, d, q, kv_cmp, cmp_off, kv_raw, raw_off, q_seq, q_pos, out, idx, raw_tok0, sink, lse,
+                        workspace, dev_status)
     if out.dtype == torch.bfloat16:
         mode = int(mode) | ATTN_OUT_BF16
     k = idx.shape[1] if idx is not None else 0
