@@ -2,7 +2,8 @@
 
 Every function here turns tensors into pointers, sizes and dtype codes and
 calls the C entry point of the same name on the current CUDA stream (or the
-one given).  All computation happens in the CUDA library.
+one given, on which the outputs that the call allocates are then allocated
+too).  All computation happens in the CUDA library.
 """
 
 from __future__ import annotations
@@ -60,10 +61,14 @@ _F32 = (torch.float32,)
 _VALUES = (torch.float32, torch.bfloat16)
 
 
-def _new(fn, shape, dtype, dtypes, device):
-    """An output of the call's own."""
+def _new(fn, shape, dtype, dtypes, device, stream=None):
+    """An output of the call's own, which belongs to the stream that the call runs on: memory of another
+    stream's may still be in use there."""
     if dtype not in dtypes:
         raise ValueError(f"{fn}: dtype {dtype}")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return torch.empty(*shape, dtype=dtype, device=device)
     return torch.empty(*shape, dtype=dtype, device=device)  # the sizes one by one: 1 us less than as a tuple
 
 
@@ -283,7 +288,7 @@ def kv_quantize_fp8(rows, out=None, stream=None):
     assert rows.dim() == 2 and rows.shape[1] == 256
     n = rows.shape[0]
     if out is None:
-        out = torch.empty(n, KV8_ROW_BYTES, dtype=torch.uint8, device=rows.device)
+        out = _new("kv_quantize_fp8", (n, KV8_ROW_BYTES), torch.uint8, _U8, rows.device, stream)
     lib = _lib.load()
     st = lib.kv_quantize_fp8(_ptr(rows), _dt(rows), n, _ptr(out), _stream(stream))
     _lib.check("kv_quantize_fp8", st)
@@ -304,9 +309,9 @@ def mxfp4_quantize(x, codes=None, bscale=None, *, stream=None):
     cs, bs = _mxfp4_shapes("mxfp4_quantize", lead, D)
     dev = _check("mxfp4_quantize", ("x", x, _VALUES, x.shape), ("codes", codes, _U8, cs), ("bscale", bscale, _U8, bs))
     if codes is None:
-        codes = _new("mxfp4_quantize", cs, torch.uint8, _U8, x.device)
+        codes = _new("mxfp4_quantize", cs, torch.uint8, _U8, x.device, stream)
     if bscale is None:
-        bscale = _new("mxfp4_quantize", bs, torch.uint8, _U8, x.device)
+        bscale = _new("mxfp4_quantize", bs, torch.uint8, _U8, x.device, stream)
     st = _lib.load().mxfp4_quantize(x.data_ptr(), _DT[x.dtype], x.numel() // D, D, codes.data_ptr(),
                                     bscale.data_ptr(), _stream(stream, dev))
     _lib.check("mxfp4_quantize", st)
@@ -321,7 +326,7 @@ def mxfp4_dequantize(codes, bscale, out=None, *, dtype=torch.bfloat16, stream=No
     dev = _check("mxfp4_dequantize", ("codes", codes, _U8, codes.shape), ("bscale", bscale, _U8, bs),
            ("out", out, _VALUES, (*lead, D)))
     if out is None:
-        out = _new("mxfp4_dequantize", (*lead, D), dtype, _VALUES, codes.device)
+        out = _new("mxfp4_dequantize", (*lead, D), dtype, _VALUES, codes.device, stream)
     st = _lib.load().mxfp4_dequantize(codes.data_ptr(), bscale.data_ptr(), out.numel() // D, D, _DT[out.dtype],
                                       out.data_ptr(), _stream(stream, dev))
     _lib.check("mxfp4_dequantize", st)
@@ -336,7 +341,7 @@ def mxfp4_matmul(a_codes, a_bscale, b_codes, b_bscale, out=None, *, dtype=torch.
            ("b_codes", b_codes, _U8, (N, half)), ("b_bscale", b_bscale, _U8, (N, half // 16)),
            ("out", out, _VALUES, (M, N)), ("dev_status", dev_status, _I32, (1,)))
     if out is None:
-        out = _new("mxfp4_matmul", (M, N), dtype, _VALUES, a_codes.device)
+        out = _new("mxfp4_matmul", (M, N), dtype, _VALUES, a_codes.device, stream)
     st = _lib.load().mxfp4_matmul(a_codes.data_ptr(), a_bscale.data_ptr(), b_codes.data_ptr(), b_bscale.data_ptr(),
                                   M, N, 2 * half, _DT[out.dtype], out.data_ptr(), _ptr(dev_status), _stream(stream, dev))
     _lib.check("mxfp4_matmul", st)
@@ -354,7 +359,7 @@ def kv_quantize_fp4(rows, out=None, *, dst=None, dev_status=None, stream=None):
     dev = _check("kv_quantize_fp4", ("rows", rows, _VALUES, (n, 256)), ("out", out, _U8, (cap, KV4_ROW_BYTES)),
            ("dst", dst, _I64, (n,)), ("dev_status", dev_status, _I32, (1,)))
     if out is None:
-        out = _new("kv_quantize_fp4", (n, KV4_ROW_BYTES), torch.uint8, _U8, rows.device)
+        out = _new("kv_quantize_fp4", (n, KV4_ROW_BYTES), torch.uint8, _U8, rows.device, stream)
     st = _lib.load().kv_quantize_fp4(rows.data_ptr(), _DT[rows.dtype], n, _ptr(dst), cap, out.data_ptr(),
                                      _ptr(dev_status), _stream(stream, dev))
     _lib.check("kv_quantize_fp4", st)
@@ -369,7 +374,7 @@ def kv_dequantize_fp4(cache, out=None, *, src=None, dtype=torch.bfloat16, dev_st
     dev = _check("kv_dequantize_fp4", ("cache", cache, _U8, (cap, KV4_ROW_BYTES)), ("out", out, _VALUES, (n, 256)),
            ("src", src, _I64, (n,)), ("dev_status", dev_status, _I32, (1,)))
     if out is None:
-        out = _new("kv_dequantize_fp4", (n, 256), dtype, _VALUES, cache.device)
+        out = _new("kv_dequantize_fp4", (n, 256), dtype, _VALUES, cache.device, stream)
     st = _lib.load().kv_dequantize_fp4(cache.data_ptr(), _ptr(src), cap, n, _DT[out.dtype], out.data_ptr(),
                                        _ptr(dev_status), _stream(stream, dev))
     _lib.check("kv_dequantize_fp4", st)
