@@ -6,9 +6,9 @@
 // is two shuffles (compared as integers: the order of non-negative floats, and an infinity or a
 // NaN stays the largest), and a warp's loads and code stores are contiguous.
 // (Sixteen values a lane halve the shuffles, but the loads were no longer contiguous: slower.)
-// Measured, quantised and back: 262144 x 64 bf16, 85 MB in 15.0 us, 5.65 TB/s, 0.86 of the copy rate;
+// Measured, quantised and back: 262144 x 64 bf16, 85 MB in 15.2 us, 5.6 TB/s, 0.86 of the copy rate;
 // 262144 main-KV rows from bf16, 180 MB in 34.5 us, 5.2 TB/s, 0.80, and back in 30 us, 6.0 TB/s, 0.92;
-// a few rows: the latency of two launches, 2.1 us.
+// a few rows: the latency of two launches, 2.4 us.
 #include <algorithm>
 
 #include "launch.cuh"

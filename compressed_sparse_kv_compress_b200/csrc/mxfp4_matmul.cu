@@ -17,8 +17,9 @@
 // is active for 44 % of the cycles.  Steps that count here: scales copied a step before their products
 // (4096^3: 50.5 -> 46.4 us), one wait and one commit a step (41.0), a row's scales loaded one
 // sector, four steps, at a time (38.2).
-// Measured (device time): 4096^3, bf16 out: 38 us, 3.6 PFLOP/s; 4096 x 512 x 4096: 10.3 us; one row
-// x 4096 x 4096: 5.5 us, 1.6 TB/s of codes; 67 x 1000 x 2080: 10.6 us.
+// Measured (device time): 4096^3, bf16 out: 40 us, 3.4 PFLOP/s, with the codes in L2 (38 to 40.6 from
+// GPU to GPU), 45 us, 3.0 PFLOP/s, with codes that are not; 4096 x 512 x 4096: 11.7 us; one row x 4096 x
+// 4096: 6.1 us, 1.5 TB/s of codes; 67 x 1000 x 2080: 10.8 us.
 #include <cuda.h>
 
 #include "launch.cuh"

@@ -430,9 +430,10 @@ CSKV_API size_t lindex_workspace_size_scan(int T, int64_t max_entries);
  *           (output 0).  Elsewhere (CSA, fp32, other H, or a plan whose splits do not fit
  *           one cluster) the bit is ignored.
  * mode | CSKV_ATTN_KV_FP8 : kv_cmp holds FP8 main-KV rows (kv_quantize_fp8: 336 bytes a
- *           row, indexed by cmp_off like the plain rows); kv_raw stays in dtype.  The rows
- *           are decoded as they are loaded, on the CUDA cores (the tensor-core kernel takes
- *           plain rows only; ignores CSKV_ATTN_PAIRS).  The workspace size is the same.
+ *           row, indexed by cmp_off like the plain rows); kv_raw stays in dtype.  bf16
+ *           queries run on the tensor cores, whose gather decodes the rows to bf16 (with
+ *           CSKV_ATTN_PAIRS as over plain rows), fp32 ones on the CUDA cores, which decode
+ *           rows as they load them.  The workspace size is the same.
  * mode | CSKV_ATTN_KV_FP4 : kv_cmp holds 4-bit main-KV rows (kv_quantize_fp4: 176 bytes a row,
  *           indexed by cmp_off like the plain rows); kv_raw stays in dtype.  bf16 queries run on
  *           the tensor cores over the rows decoded to bf16 (exact), fp32 ones on the CUDA cores;
